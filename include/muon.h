@@ -340,6 +340,63 @@ muon_status muon_step_profiled(const muon_matrix* mats, int32_t count, const muo
 muon_status muon_step_events(const muon_matrix* mats, int32_t count, const muon_params* p,
                              void* ws, size_t ws_bytes, void* stream, void* const* events);
 
+/* ---- Products grouped by expert -----------------------------------------
+ *
+ * For a mixture-of-experts layer whose rows are sorted by expert: expert e
+ * owns rows offsets[e] .. offsets[e+1] - 1 of x, y, dy and dx, and the n x k
+ * weight W_e. The sizes stay on the device, so a router can write the offsets
+ * and the products follow without the host reading them.
+ *   dtype      BF16 or F16: type of x, W, y, dy and dx; sums are fp32 and each
+ *              result is rounded once
+ *   experts    0..1024
+ *   tokens     rows of x and y (0..2^31 - 1); n, k >= 1
+ *   ldx        row stride of x and dx (>= k), ldy of y and dy (>= n), ldw of
+ *              W_e (>= k), w_stride from expert to expert (>= (n-1) ldw + k;
+ *              not read when there is one), all in elements. Data pointers
+ *              are 16-byte aligned and every stride is a multiple of 16 bytes
+ *              (MUON_ERR_ALIGN otherwise); n and k themselves may be odd.
+ *   offsets    experts + 1 non-decreasing device int32 within 0..tokens. An
+ *              expert may be empty; rows before offsets[0] and from
+ *              offsets[experts] on belong to no expert: they are not read,
+ *              and the rows of y or dx at these places keep their values. An
+ *              entry out of range or smaller than the one before is clamped
+ *              and reported as MUON_ERR_INVALID_ARG to dev_status (the
+ *              results are then unspecified, but no access leaves its matrix)
+ *   dev_status optional device int32 for deferred errors, not cleared by the
+ *              library (as in muon_params)
+ * Outputs may not alias inputs. A row's result depends on its own row and its
+ * expert's weight alone, whatever (NaN included) the other rows hold. */
+typedef struct {
+  muon_dtype dtype;
+  int32_t experts;
+  int64_t tokens;
+  int64_t n;
+  int64_t k;
+  int64_t ldx;
+  int64_t ldy;
+  int64_t ldw;
+  int64_t w_stride;
+  const int32_t* offsets;
+  int32_t* dev_status;
+} muon_grouped;
+
+/* y[r,:] = x[r,:] W_e^T for the rows r of every expert e. */
+muon_status grouped_matmul(const muon_grouped* g, const void* x, const void* w, void* y, void* stream);
+
+/* dx[r,:] = dy[r,:] W_e: the gradient of grouped_matmul for its rows. */
+muon_status grouped_matmul_dx(const muon_grouped* g, const void* dy, const void* w, void* dx, void* stream);
+
+/* Workspace bytes of grouped_matmul_dw (0 if experts is out of range). */
+size_t grouped_workspace_size(int32_t experts);
+
+/* dW_e = alpha sum_r dy[r,:]^T x[r,:] + beta dW_e over the rows r of expert e:
+ * the gradient of grouped_matmul for its weights, in dw_dtype (F32, or the
+ * type of dy and x) with strides ldw and w_stride. beta = 0 does not read dW
+ * (an expert without rows then gets zeros); beta = mu with an fp32 momentum
+ * is the first line of Eq. (1), M <- mu M + G, without a gradient in memory. */
+muon_status grouped_matmul_dw(const muon_grouped* g, const void* dy, const void* x, void* dw, muon_dtype dw_dtype,
+                              float alpha, float beta, void* ws, size_t ws_bytes, void* stream);
+
 /* Number of kernels this library has queued from the calling thread since it
  * was loaded (monotonic; for counting launches inside a timed region). */
 int64_t muon_kernel_launch_count(void);

@@ -911,6 +911,72 @@ muon_status muon_apply_update(const muon_matrix* mats, int32_t count, const muon
   });
 }
 
+namespace {
+
+// Shapes, strides and types of a grouped call; pointers are checked by each
+// entry point. out_bytes: element size of the weights' side (dW may be fp32).
+muon_status check_grouped(const muon_grouped* g, int w_bytes, Op* t) {
+  if (!g) return MUON_ERR_INVALID_ARG;
+  if (g->dtype != MUON_BF16 && g->dtype != MUON_F16) return MUON_ERR_DTYPE;
+  op_of(g->dtype, t);
+  if (g->experts < 0 || g->experts > grouped_max_experts() || g->tokens < 0 || g->tokens > INT32_MAX || g->n < 1 ||
+      g->k < 1 || g->n > INT32_MAX - 512 || g->k > INT32_MAX - 512)
+    return MUON_ERR_SHAPE;
+  if (g->ldx < g->k || g->ldy < g->n || g->ldw < g->k) return MUON_ERR_SHAPE;
+  if (g->experts > 1 && g->w_stride < (g->n - 1) * g->ldw + g->k) return MUON_ERR_SHAPE;  // experts may not overlap
+  if (g->ldx % 8 || g->ldy % 8 || g->ldw * w_bytes % 16 || (g->experts > 1 && g->w_stride * w_bytes % 16))
+    return MUON_ERR_ALIGN;
+  if (g->dev_status && (reinterpret_cast<uintptr_t>(g->dev_status) & 3u)) return MUON_ERR_ALIGN;
+  return MUON_OK;
+}
+
+GroupedDesc grouped_desc(const muon_grouped* g, Op t) {
+  return GroupedDesc{t,      g->experts, g->tokens,   g->n,       g->k,         g->ldx,
+                     g->ldy, g->ldw,     g->w_stride, g->offsets, g->dev_status};
+}
+
+muon_status grouped_rows_impl(const muon_grouped* g, const void* x, const void* w, void* y, bool mn, void* stream) {
+  Op t;
+  TRY(check_grouped(g, 2, &t));
+  if (g->experts == 0 || g->tokens == 0) return MUON_OK;
+  if (!x || !w || !y || !g->offsets) return MUON_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || (reinterpret_cast<uintptr_t>(g->offsets) & 3u))
+    return MUON_ERR_ALIGN;
+  const GroupedDesc d = grouped_desc(g, t);
+  if (!grouped_fits(d)) return MUON_ERR_SHAPE;
+  return grouped_rows(d, x, w, y, mn, timeout_ns(), static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+muon_status grouped_matmul(const muon_grouped* g, const void* x, const void* w, void* y, void* stream) {
+  return grouped_rows_impl(g, x, w, y, false, stream);
+}
+
+muon_status grouped_matmul_dx(const muon_grouped* g, const void* dy, const void* w, void* dx, void* stream) {
+  return grouped_rows_impl(g, dy, w, dx, true, stream);
+}
+
+size_t grouped_workspace_size(int32_t experts) {
+  return experts < 0 || experts > grouped_max_experts() ? 0 : grouped_ws(experts);
+}
+
+muon_status grouped_matmul_dw(const muon_grouped* g, const void* dy, const void* x, void* dw, muon_dtype dw_dtype,
+                              float alpha, float beta, void* ws, size_t ws_bytes, void* stream) {
+  Op t, ot;
+  TRY(check_grouped(g, dw_dtype == MUON_F32 ? 4 : 2, &t));
+  if ((dw_dtype != MUON_F32 && dw_dtype != g->dtype) || !op_of(dw_dtype, &ot)) return MUON_ERR_DTYPE;
+  if (!std::isfinite(alpha) || !std::isfinite(beta)) return MUON_ERR_INVALID_ARG;
+  if (g->experts == 0) return MUON_OK;
+  if (!dw || !g->offsets || (g->tokens > 0 && (!dy || !x))) return MUON_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(dw) || (reinterpret_cast<uintptr_t>(g->offsets) & 3u))
+    return MUON_ERR_ALIGN;
+  if (!ws || ws_bytes < grouped_ws(g->experts)) return MUON_ERR_WORKSPACE;
+  const GroupedDesc d = grouped_desc(g, t);
+  if (!grouped_fits(d)) return MUON_ERR_SHAPE;
+  return grouped_dw(d, dy, x, dw, ot, alpha, beta, ws, timeout_ns(), static_cast<cudaStream_t>(stream));
+}
+
 int64_t muon_kernel_launch_count(void) { return counters().launches; }
 
 }  // extern "C"

@@ -1079,6 +1079,11 @@ int num_sms() {
   return n;
 }
 
+bool make_tensor_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
+                     int64_t bstride, int box_outer) {
+  return make_map(m, t, base, inner, outer, batch, ld, bstride, box_outer);
+}
+
 void set_gemm_pair_mode(int pair) { g_pair_mode = pair == 1 ? 1 : 2; }
 
 namespace {

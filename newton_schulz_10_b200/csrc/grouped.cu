@@ -1,0 +1,786 @@
+// Matrix products grouped by expert with ragged sizes, on sm_100a.
+//
+// The rows of x (tokens x k) are sorted by expert; expert e owns rows
+// offsets[e] .. offsets[e+1] (device int32, so the sizes never reach the
+// host). With W_e the e-th n x k weight:
+//   grouped_matmul     y[r,:]  = x[r,:] W_e^T          (ROWS, W read K-major)
+//   grouped_matmul_dx  dx[r,:] = dy[r,:] W_e           (ROWS, W read MN-major)
+//   grouped_matmul_dw  dW_e    = alpha dy_e^T x_e + beta dW_e   (DW)
+//
+// One persistent, warp-specialised launch over every expert's tiles (the
+// roles and the CTA-pair mainloop are those of the Newton-Schulz GEMM): a
+// cluster of two CTAs owns a tile of 256 x NT, tcgen05.mma cta_group::2 with
+// M = 256, operands by TMA with 128-byte swizzle, two fp32 accumulators of
+// 256 TMEM columns so that the epilogue of one tile overlaps the mainloop of
+// the next.
+//
+// ROWS computes the transposed product: the expert's weights are the M side
+// (always full tiles) and its tokens the N side, because the instruction
+// takes any N that is a multiple of 32: a ragged group wastes at most 31
+// columns instead of up to 255 rows, and a decoding batch of a few tokens
+// streams each weight once through a narrow tile. NT, the widest token tile
+// of a launch, is 32, 64, 128 or 256; a narrow one leaves room for more
+// stages. Rows of neighbouring experts that a box reads past the end of a
+// group only reach accumulator columns that are never stored.
+//
+// DW has the tokens on the K side, where a neighbour's rows would enter the
+// sums (and a NaN among them would spoil them): a small launch first writes,
+// per expert, copies of the two operands' tensor maps whose row count ends
+// with the expert's last row, so that the copies themselves fill zeros behind
+// it. An expert without rows gets beta dW_e (0 when beta is 0).
+//
+// Every wait is bounded as in the Newton-Schulz GEMM; offsets are clamped to
+// 0..tokens before use, and a decreasing or out-of-range entry is reported as
+// MUON_ERR_INVALID_ARG.
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace muon {
+
+namespace grp {
+
+constexpr int BM = 128, BK = 64;  // BM: rows of the M side per CTA
+constexpr int TILE_M = 2 * BM;
+constexpr int UMMA_K = 16;
+constexpr int EPI_WARP0 = 4;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int TMEM_COLS = 512;
+constexpr int ACC_COLS = 256;
+constexpr int kMaxExperts = 1024;
+constexpr uint64_t DRAIN_NS = 1000000000ull;
+
+enum : int { ROWS = 0, DW = 1 };
+
+template <int MODE, int NT>
+struct Cfg {
+  static constexpr int A_STAGE = BM * BK * 2;
+  static constexpr int B_STAGE = (NT / 2) * BK * 2;
+  static constexpr int TX_BYTES = 2 * (A_STAGE + B_STAGE);  // per stage, both CTAs
+  static constexpr int STAGES = NT == 256 ? 6 : NT == 128 ? 8 : NT == 64 ? 9 : 10;
+  static constexpr int EPI_BUF = MODE == ROWS ? 2048 : 4096;  // one 32x32 block per warp (16-bit, fp32)
+  static constexpr int TABLE = MODE == ROWS ? (kMaxExperts + 1 + 32) * 4 : 0;
+  static constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * EPI_BUF + TABLE + (2 * STAGES + 5) * 8 + 64;
+  static_assert(SMEM <= 232448, "exceeds the opt-in shared memory of one sm_100 CTA");
+};
+
+struct Params {
+  CUtensorMap mapA;       // ROWS: W; DW: dy (the copies per expert are in `clipped`)
+  CUtensorMap mapB;       // ROWS: x or dy; DW: x
+  CUtensorMap* clipped;   // DW: [experts][2]
+  const int32_t* offsets;
+  void* out;
+  long long ldo, so;      // row stride; DW: expert stride
+  int tokens, experts;
+  int M, N, K;            // ROWS: M = features out, K = features in; DW: M = n, N = k
+  int a_mn;               // ROWS: W read MN-major
+  int vec;                // DW: 16-byte accesses of out are aligned
+  float alpha, beta;      // DW
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+struct Span {
+  int begin, end;
+};
+
+// Rows of expert e, clamped to 0..tokens.
+__device__ __forceinline__ Span span_of(const Params& p, int e) {
+  int s = __ldg(p.offsets + e), t = __ldg(p.offsets + e + 1);
+  s = s < 0 ? 0 : s > p.tokens ? p.tokens : s;
+  t = t < s ? s : t > p.tokens ? p.tokens : t;
+  return Span{s, t};
+}
+
+struct Tile {
+  int e;
+  int m0;        // first row of the pair's M side
+  int n0;        // ROWS: first token; DW: first column of the pair's N side
+  int nvalid;    // ROWS: tokens of this tile
+  int n_mma;     // N of the instruction
+  int t0, t1;    // DW: the expert's rows (the K side)
+  int nkb;       // k-blocks
+};
+
+// Token tiles of a group of `cnt` rows, and their width: equal shares of a
+// multiple of 32 tokens while there are few (two tiles of 160 rather than
+// 256 and 44), full tiles for long groups (where rounding the shares up
+// could leave a last tile without rows).
+template <int NT>
+__device__ __forceinline__ int token_tiles(int cnt) { return (cnt + NT - 1) / NT; }
+template <int NT>
+__device__ __forceinline__ int token_width(int cnt, int tiles) {
+  if (tiles > 4) return NT;
+  return ((cnt + tiles - 1) / tiles + 31) & ~31;
+}
+
+template <int MODE, int NT>
+__device__ __forceinline__ Tile decode(const Params& p, const int* tile_begin, int tile, int mt, int ntl) {
+  Tile t;
+  if (MODE == ROWS) {
+    const int tt = tile / mt;
+    t.m0 = (tile - tt * mt) * TILE_M;
+    int lo = 0, hi = p.experts - 1;  // the last expert whose first token tile is <= tt
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tile_begin[mid] <= tt) lo = mid; else hi = mid - 1;
+    }
+    t.e = lo;
+    const Span s = span_of(p, lo);
+    const int cnt = s.end - s.begin, tiles = token_tiles<NT>(cnt);
+    const int w = token_width<NT>(cnt, tiles);
+    t.n0 = s.begin + (tt - tile_begin[lo]) * w;
+    const int left = s.end - t.n0;
+    t.nvalid = left < w ? left : w;
+    t.n_mma = (t.nvalid + 31) & ~31;
+    t.t0 = t.t1 = 0;
+    t.nkb = (p.K + BK - 1) / BK;
+  } else {
+    const int per = mt * ntl;
+    t.e = tile / per;
+    const int r = tile - t.e * per;
+    t.m0 = (r / ntl) * TILE_M;
+    t.n0 = (r % ntl) * NT;
+    t.nvalid = 0;
+    t.n_mma = NT;
+    const Span s = span_of(p, t.e);
+    t.t0 = s.begin;
+    t.t1 = s.end;
+    t.nkb = (s.end - s.begin + BK - 1) / BK;
+  }
+  return t;
+}
+
+__device__ __forceinline__ uint32_t sw64(int r, int c) {
+  return (uint32_t)(r * 64 + ((((c >> 3) ^ (r >> 1)) & 3) << 4) + ((c & 7) << 1));
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
+  const uint32_t addr = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(addr, parity)) {
+    if (globaltimer_ns() - t0 > DRAIN_NS) {
+      report(status, MUON_ERR_TIMEOUT);
+      break;
+    }
+  }
+}
+
+// Early exit of a pair: wait until every operand copy that either CTA issued
+// has landed. cnt: k-blocks issued by the leader's A and B producers and the
+// follower's. Blocks before max(cnt) - STAGES have been consumed; each later
+// one occupies its own stage, whose barrier is settled for the copies that
+// were never issued and then waited on.
+template <int MODE, int NT>
+__device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
+  using Cf = Cfg<MODE, NT>;
+  const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
+  const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
+  int hi = 0;
+  for (int x = 0; x < 4; ++x) hi = c[x] > hi ? c[x] : hi;
+  for (int j = hi > Cf::STAGES ? hi - Cf::STAGES : 0; j < hi; ++j) {
+    uint32_t issued = 0;
+    for (int x = 0; x < 4; ++x)
+      if (j < c[x]) issued += bytes[x];
+    uint64_t* bar = &full[j % Cf::STAGES];
+    if (j < c[0]) {
+      if (issued < (uint32_t)Cf::TX_BYTES) mbar_complete_tx(bar, Cf::TX_BYTES - issued);
+    } else {
+      mbar_arrive_expect_tx(bar, issued);
+    }
+    drain_wait(bar, (uint32_t)((j / Cf::STAGES) & 1), status);
+  }
+}
+
+__device__ __forceinline__ void fence_map_acquire(const CUtensorMap* m) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+// One thread per expert and operand: the operand's tensor map with its row
+// count cut at the expert's last row.
+__global__ void __launch_bounds__(128) clip_maps(const __grid_constant__ Params p) {
+  grid_dependency_wait();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  const int e = i >> 1;
+  if (e >= p.experts) return;
+  const int raw0 = __ldg(p.offsets + e), raw1 = __ldg(p.offsets + e + 1);
+  const Span s = span_of(p, e);
+  if ((raw0 != s.begin || raw1 != s.end) && !(i & 1)) report(p.status, MUON_ERR_INVALID_ARG);
+  if (s.end <= s.begin) return;  // no copy reads this expert's maps
+  CUtensorMap* m = p.clipped + i;
+  const uint4* src = reinterpret_cast<const uint4*>((i & 1) ? &p.mapB : &p.mapA);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(m)[k] = src[k];
+  asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(__cvta_generic_to_global(m)),
+               "r"(s.end)
+               : "memory");
+  asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+}
+
+template <typename O>
+__device__ __forceinline__ float out_to_f(O x);
+template <>
+__device__ __forceinline__ float out_to_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float out_to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float out_to_f<__half>(__half x) { return __half2float(x); }
+template <typename O>
+__device__ __forceinline__ O f_to_out(float x);
+template <>
+__device__ __forceinline__ float f_to_out<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 f_to_out<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half f_to_out<__half>(float x) { return __float2half_rn(x); }
+
+// Four consecutive elements of the output, aligned to 4 elements.
+template <typename O>
+__device__ __forceinline__ float4 load_out4(const O* p) {
+  if constexpr (std::is_same<O, float>::value) {
+    return *reinterpret_cast<const float4*>(p);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = Elem<O>::unpack2(u.x), b = Elem<O>::unpack2(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+template <typename O>
+__device__ __forceinline__ void store_out4(O* p, float4 v) {
+  if constexpr (std::is_same<O, float>::value) {
+    *reinterpret_cast<float4*>(p) = v;
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(Elem<O>::pack2(v.x, v.y), Elem<O>::pack2(v.z, v.w));
+  }
+}
+
+template <typename T, typename O, int MODE, int NT>
+__global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_constant__ Params p) {
+  using Cf = Cfg<MODE, NT>;
+  constexpr int STAGES = Cf::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * Cf::A_STAGE;
+  uint8_t* sEpi = sB + STAGES * Cf::B_STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + EPI_WARPS * Cf::EPI_BUF);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + STAGES;
+  uint64_t* tfull = bars + 2 * STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* issued_cnt = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int* table = reinterpret_cast<int*>(tmem_slot + 8);  // ROWS: first token tile of each expert, then scan scratch
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();  // 0 = leader
+  const int unit = (int)(blockIdx.x >> 1), units = (int)(gridDim.x >> 1);
+  auto raise_peer = [&]() { st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], EPI_WARPS * 2);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) issued_cnt[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  if (MODE == ROWS && warp == 0 && lane == 0) {
+    prefetch_tmap(&p.mapA);
+    prefetch_tmap(&p.mapB);
+  }
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int mt = (p.M + TILE_M - 1) / TILE_M;
+  const int ntl = MODE == DW ? (p.N + NT - 1) / NT : 1;
+  int total;
+  if (MODE == ROWS) {
+    // Prefix sum of the experts' token tiles: each thread sums up to three
+    // consecutive experts, then warps, then the block.
+    constexpr int PER = (kMaxExperts + THREADS - 1) / THREADS;
+    int* wsum = table + kMaxExperts + 1;
+    const int e0 = threadIdx.x * PER;
+    int c[PER], sum = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      c[i] = 0;
+      if (e0 + i < p.experts) {
+        const Span s = span_of(p, e0 + i);
+        bad |= s.begin != __ldg(p.offsets + e0 + i) || s.end != __ldg(p.offsets + e0 + i + 1);
+        c[i] = token_tiles<NT>(s.end - s.begin);
+      }
+      sum += c[i];
+    }
+    if (bad && blockIdx.x == 0) report(p.status, MUON_ERR_INVALID_ARG);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int base = incl - sum, all = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) base += wsum[w];
+      all += wsum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (e0 + i < p.experts) table[e0 + i] = base;
+      base += c[i];
+    }
+    total = all * mt;
+  } else {
+    total = p.experts * mt * ntl;
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // barriers initialised in both CTAs, table written
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint64_t budget = p.timeout_ns;
+
+  if ((warp == 0 || warp == 3) && lane == 0) {
+    // TMA producers: warp 0 the M side (and the leader's byte count), warp 3
+    // the N side; both take part in every phase of every stage.
+    const bool issues_a = warp == 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    int last_e = -1;
+    bool ok = true;
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
+      const int am0 = t.m0 + (int)rank * BM;
+      const int bn0 = t.n0 + (int)rank * (t.n_mma / 2);
+      const CUtensorMap* map = issues_a ? &p.mapA : &p.mapB;
+      if (MODE == DW) {
+        map = p.clipped + 2 * t.e + (issues_a ? 0 : 1);
+        if (t.e != last_e && t.nkb > 0) {
+          fence_map_acquire(map);
+          last_e = t.e;
+        }
+      }
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status)) {
+          raise_peer();
+          ok = false;
+          break;
+        }
+        if (issues_a && rank == 0) mbar_arrive_expect_tx(&full[stage], Cf::TX_BYTES);
+        uint8_t* a = sA + stage * Cf::A_STAGE;
+        uint8_t* b = sB + stage * Cf::B_STAGE;
+        const int k0 = kb * BK;
+        if (MODE == ROWS) {
+          if (!issues_a) {
+            tma_load_3d_pair(b, map, k0, bn0, 0, &full[stage]);
+          } else if (!p.a_mn) {
+            tma_load_3d_pair(a, map, k0, am0, t.e, &full[stage]);
+          } else {
+            tma_load_3d_pair(a, map, am0, k0, t.e, &full[stage]);
+            tma_load_3d_pair(a + 8192, map, am0 + 64, k0, t.e, &full[stage]);
+          }
+        } else {
+          uint8_t* d = issues_a ? a : b;
+          const int c0 = issues_a ? am0 : bn0;
+          constexpr int NB = NT / 2 / 64;
+          tma_load_3d_pair(d, map, c0, t.t0 + k0, 0, &full[stage]);
+          if (issues_a || NB > 1) tma_load_3d_pair(d + 8192, map, c0 + 64, t.t0 + k0, 0, &full[stage]);
+        }
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    const uint32_t slot = smem_u32(const_cast<int*>(issued_cnt + 2 * rank + (issues_a ? 0 : 1)));
+    st_cluster_u32(mapa_shared(slot, 0), (uint32_t)issued);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // MMA issuer (the leader issues for the pair)
+    int stage = 0;
+    uint32_t phase = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB);
+    constexpr int fmt = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    const int a_mn = MODE == DW ? 1 : p.a_mn;
+    constexpr int b_mn = MODE == DW ? 1 : 0;
+    // K-major: 8-row groups 1024 B apart, one K step = 32 B inside the swizzle
+    // atom. MN-major: 64-element MN atoms 8 KB apart, 8-row K groups 1024 B
+    // apart, one K step of 16 rows = 2048 B.
+    const uint32_t a_kstep = a_mn ? 2048u : 32u, b_kstep = b_mn ? 2048u : 32u;
+    const uint64_t a_hi = smem_desc_sw128(0, a_mn ? 8192u : 16u, 1024);
+    const uint64_t b_hi = smem_desc_sw128(0, b_mn ? 8192u : 16u, 1024);
+    bool ok = true;
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
+      const uint32_t idesc = idesc_f16(fmt, a_mn, b_mn, TILE_M, t.n_mma);
+      if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, budget, p.status)) {
+        raise_peer();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, budget, p.status)) {
+          raise_peer();
+          ok = false;
+          break;
+        }
+        const uint32_t a_lo = (a_base + stage * Cf::A_STAGE) >> 4, b_lo = (b_base + stage * Cf::B_STAGE) >> 4;
+#pragma unroll
+        for (int k = 0; k < BK / UMMA_K; ++k)
+          umma_f16_pair(d_tmem, a_hi | (uint64_t)(a_lo + k * (a_kstep >> 4)), b_hi | (uint64_t)(b_lo + k * (b_kstep >> 4)),
+                        idesc, kb != 0 || k != 0);
+        umma_commit_pair(&empty[stage], 0x3);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      umma_commit_pair(&tfull[acc], 0x3);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    umma_commit_pair(drain, 0x3);
+    drain_wait(drain, 0, p.status);
+  } else if (warp == 1 && lane == 0) {
+    drain_wait(drain, 0, p.status);  // the follower: no MMA reads its shared memory or writes its TMEM any more
+  } else if (warp >= EPI_WARP0) {
+    const int e = warp - EPI_WARP0;
+    const int q = warp & 3;   // TMEM lane quarter
+    const int half = e >> 2;  // which of the alternating 32-column chunks
+    uint8_t* const sd = sEpi + e * Cf::EPI_BUF;
+    const uint32_t sd_a = smem_u32(sd);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = unit; tile < total; tile += units) {
+      const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
+      const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, budget, p.status);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) raise_peer();
+        break;
+      }
+      tc_fence_after();
+      const int r0 = t.m0 + (int)rank * BM + q * 32;  // first M-side row of this warp
+      const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + acc * ACC_COLS;
+      if (MODE == ROWS) {
+        // block: lanes = features r0.., columns = tokens; stored transposed
+        O* const out = reinterpret_cast<O*>(p.out);
+        for (int c = half * 32; c < t.nvalid; c += 64) {
+          if (r0 >= p.M) break;  // warp-uniform
+          uint32_t f0[16], f1[16];
+          tmem_ld_16x256_x4(trow + c, f0);
+          tmem_ld_16x256_x4(trow + c + (16u << 16), f1);
+          tmem_wait_ld();
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int x = 4 * i + 2 * k;
+              pk[4 * k + i] = Elem<T>::pack2(__uint_as_float(f0[x]), __uint_as_float(f0[x + 1]));
+              pk[8 + 4 * k + i] = Elem<T>::pack2(__uint_as_float(f1[x]), __uint_as_float(f1[x + 1]));
+            }
+          __syncwarp();  // the previous chunk has been read
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            stsm_x4_trans(sd_a + sw64(lane, 16 * (k >> 1) + 8 * (k & 1)), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2],
+                          pk[4 * k + 3]);
+          __syncwarp();
+          // rows of 32 features: four lanes a row, 16 bytes a lane
+          const int f = r0 + (lane & 3) * 8;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int tk = 8 * j + (lane >> 2);
+            if (c + tk >= t.nvalid || f >= p.M) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(tk, (lane & 3) * 8));
+            O* d = out + (long long)(t.n0 + c + tk) * p.ldo + f;
+            if (f + 8 <= p.M) {
+              *reinterpret_cast<uint4*>(d) = v;
+            } else {
+              const O* h = reinterpret_cast<const O*>(&v);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if (f + x < p.M) d[x] = h[x];
+            }
+          }
+        }
+      } else {
+        // block: lanes = rows of dW_e, columns = its columns; staged so that
+        // eight lanes cover a row of 32 consecutive elements
+        O* const out = reinterpret_cast<O*>(p.out) + (long long)t.e * p.so;
+        for (int c = half * 32; c < NT; c += 64) {
+          const int c0 = t.n0 + c;
+          if (r0 >= p.M || c0 >= p.N) break;  // warp-uniform
+          const int cc = c0 + (lane & 7) * 4;
+          float4 old[8];
+          if (p.beta != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int r = r0 + 4 * j + (lane >> 3);
+              old[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (r >= p.M || cc >= p.N) continue;
+              const O* d = out + (long long)r * p.ldo + cc;
+              if (p.vec && cc + 4 <= p.N) {
+                old[j] = load_out4<O>(d);
+              } else {
+                float* o = &old[j].x;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  if (cc + x < p.N) o[x] = out_to_f<O>(d[x]);
+              }
+            }
+          }
+          uint32_t raw[32];
+          if (t.nkb > 0) {
+            tmem_ld_32x32(trow + c, raw);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) raw[x] = 0u;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(sd + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                make_uint4(raw[4 * k], raw[4 * k + 1], raw[4 * k + 2], raw[4 * k + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int rr = 4 * j + (lane >> 3);
+            const int r = r0 + rr;
+            if (r >= p.M || cc >= p.N) continue;
+            float4 v = *reinterpret_cast<const float4*>(sd + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            v.x *= p.alpha; v.y *= p.alpha; v.z *= p.alpha; v.w *= p.alpha;
+            if (p.beta != 0.f) {
+              v.x = fmaf(p.beta, old[j].x, v.x); v.y = fmaf(p.beta, old[j].y, v.y);
+              v.z = fmaf(p.beta, old[j].z, v.z); v.w = fmaf(p.beta, old[j].w, v.w);
+            }
+            O* d = out + (long long)r * p.ldo + cc;
+            if (p.vec && cc + 4 <= p.N) {
+              store_out4<O>(d, v);
+            } else {
+              const float* o = &v.x;
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (cc + x < p.N) d[x] = f_to_out<O>(o[x]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank != 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+        else mbar_arrive(&tempty[acc]);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while its pair still signals it
+  tc_fence_after();
+  if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<MODE, NT>(full, issued_cnt, p.status);
+  __syncwarp();
+  cluster_sync();
+  if (warp == 2) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+}  // namespace grp
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+// Co-resident clusters of one form of the kernel on the current device.
+template <typename T, typename O, int MODE, int NT>
+int pair_units() {
+  static std::mutex mu;
+  static int per_device[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return 0;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  int& units = per_device[dev];
+  if (units == 0) {
+    const void* fn = (const void*)grp::grouped_kernel<T, O, MODE, NT>;
+    constexpr int smem = grp::Cfg<MODE, NT>::SMEM;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    int u = num_sms() / 2;
+    cudaLaunchConfig_t q = {};
+    q.gridDim = dim3(2 * u);
+    q.blockDim = dim3(grp::THREADS);
+    q.dynamicSmemBytes = smem;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = 2;
+    a[0].val.clusterDim.y = 1;
+    a[0].val.clusterDim.z = 1;
+    q.attrs = a;
+    q.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, fn, &q) == cudaSuccess && clusters > 0 && clusters < u) u = clusters;
+    cudaGetLastError();
+    units = u;
+  }
+  return units;
+}
+
+template <typename T, typename O, int MODE, int NT>
+muon_status launch_grouped(const grp::Params& p, long long tiles, cudaStream_t s) {
+  const int units = pair_units<T, O, MODE, NT>();
+  if (units <= 0) return MUON_ERR_CUDA;
+  const int use = tiles < units ? (int)tiles : units;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * use);
+  cfg.blockDim = dim3(grp::THREADS);
+  cfg.dynamicSmemBytes = grp::Cfg<MODE, NT>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  counters().launches += 1;
+  return cudaLaunchKernelEx(&cfg, grp::grouped_kernel<T, O, MODE, NT>, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+template <typename T>
+muon_status rows_typed(grp::Params& p, int nt, cudaStream_t s) {
+  const long long mt = (p.M + grp::TILE_M - 1) / grp::TILE_M;
+  const long long tiles = mt * ((p.tokens + nt - 1) / nt + p.experts);  // at least the tiles there are
+  switch (nt) {
+    case 32: return launch_grouped<T, T, grp::ROWS, 32>(p, tiles, s);
+    case 64: return launch_grouped<T, T, grp::ROWS, 64>(p, tiles, s);
+    case 128: return launch_grouped<T, T, grp::ROWS, 128>(p, tiles, s);
+    default: return launch_grouped<T, T, grp::ROWS, 256>(p, tiles, s);
+  }
+}
+
+template <typename T, typename O>
+muon_status dw_typed(const grp::Params& p, cudaStream_t s) {
+  const int threads = 128, blocks = (2 * p.experts + threads - 1) / threads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  counters().launches += 1;
+  if (cudaLaunchKernelEx(&cfg, grp::clip_maps, p) != cudaSuccess) return MUON_ERR_CUDA;
+  const long long mt = (p.M + grp::TILE_M - 1) / grp::TILE_M, nt = (p.N + 255) / 256;
+  return launch_grouped<T, O, grp::DW, 256>(p, mt * nt * p.experts, s);
+}
+
+}  // namespace
+
+int grouped_max_experts() { return grp::kMaxExperts; }
+
+bool grouped_fits(const GroupedDesc& g) {
+  // the narrowest token tile and both tile counts of the widest direction
+  const double mt = (double)((g.n > g.k ? g.n : g.k) / grp::TILE_M + 1);
+  const double rows = mt * ((double)g.tokens / 32 + g.experts + 1);
+  const double dw = (double)g.experts * (g.n / 256 + 1) * (g.k / 256 + 1);
+  return rows < 2147483647.0 && dw < 2147483647.0;
+}
+
+// Token tile of a launch: the smallest width that holds twice the average
+// group, so that most groups are one tile; wider tiles read each weight fewer
+// times, narrower ones keep more stages of weights in flight.
+static int token_tile(int64_t tokens, int experts) {
+  const int64_t want = 2 * ((tokens + experts - 1) / experts);
+  return want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+}
+
+muon_status grouped_rows(const GroupedDesc& g, const void* x, const void* w, void* y, bool mn, uint64_t timeout_ns,
+                         cudaStream_t s) {
+  // mn: dx = dy W (x holds dy, y holds dx), else y = x W^T
+  grp::Params p;
+  memset(&p, 0, sizeof(p));
+  p.M = (int)(mn ? g.k : g.n);
+  p.K = (int)(mn ? g.n : g.k);
+  const int64_t ldi = mn ? g.ldy : g.ldx;
+  p.ldo = mn ? g.ldx : g.ldy;
+  const int nt = token_tile(g.tokens, g.experts);
+  if (!make_tensor_map(&p.mapA, g.type, w, g.k, g.n, g.experts, g.ldw, g.w_stride, mn ? 64 : grp::BM)) return MUON_ERR_CUDA;
+  if (!make_tensor_map(&p.mapB, g.type, x, p.K, g.tokens, 1, ldi, 0, nt / 2)) return MUON_ERR_CUDA;
+  p.offsets = g.offsets;
+  p.out = y;
+  p.tokens = (int)g.tokens;
+  p.experts = g.experts;
+  p.a_mn = mn ? 1 : 0;
+  p.status = g.status;
+  p.timeout_ns = timeout_ns;
+  return g.type == Op::BF16 ? rows_typed<__nv_bfloat16>(p, nt, s) : rows_typed<__half>(p, nt, s);
+}
+
+size_t grouped_ws(int experts) { return (size_t)experts * 2 * sizeof(CUtensorMap) + 128; }
+
+muon_status grouped_dw(const GroupedDesc& g, const void* dy, const void* x, void* dw, Op out, float alpha, float beta,
+                       void* ws, uint64_t timeout_ns, cudaStream_t s) {
+  grp::Params p;
+  memset(&p, 0, sizeof(p));
+  p.M = (int)g.n;
+  p.N = (int)g.k;
+  if (g.tokens > 0) {  // without rows no copy reads the maps
+    if (!make_tensor_map(&p.mapA, g.type, dy, g.n, g.tokens, 1, g.ldy, 0, 64)) return MUON_ERR_CUDA;
+    if (!make_tensor_map(&p.mapB, g.type, x, g.k, g.tokens, 1, g.ldx, 0, 64)) return MUON_ERR_CUDA;
+  }
+  p.clipped = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
+  p.offsets = g.offsets;
+  p.out = dw;
+  p.ldo = g.ldw;
+  p.so = g.w_stride;
+  p.tokens = (int)g.tokens;
+  p.experts = g.experts;
+  p.vec = 1;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.status = g.status;
+  p.timeout_ns = timeout_ns;
+  if (g.type == Op::BF16)
+    return out == Op::F32 ? dw_typed<__nv_bfloat16, float>(p, s) : dw_typed<__nv_bfloat16, __nv_bfloat16>(p, s);
+  return out == Op::F32 ? dw_typed<__half, float>(p, s) : dw_typed<__half, __half>(p, s);
+}
+
+}  // namespace muon

@@ -81,6 +81,31 @@ muon_status simt_gemm(const GemmDesc& g, cudaStream_t s);
 
 int num_sms();
 
+// Tensor map over [batch][outer][inner] with row stride ld and batch stride
+// (elements), box {64, box_outer, 1}, 128-byte swizzle, zeros out of range.
+bool make_tensor_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
+                     int64_t bstride, int box_outer);
+
+// Products grouped by expert (grouped.cu). Checked arguments of one call:
+// x is tokens x k (ldx), y / dy tokens x n (ldy), W_e n x k (ldw, w_stride).
+struct GroupedDesc {
+  Op type;  // BF16 or F16
+  int experts;
+  int64_t tokens, n, k, ldx, ldy, ldw, w_stride;
+  const int32_t* offsets;
+  int* status;
+};
+int grouped_max_experts();
+// True when every tile of a call can be numbered in 31 bits.
+bool grouped_fits(const GroupedDesc& g);
+// mn = false: y = x W^T; mn = true: dx (y) = dy (x) W.
+muon_status grouped_rows(const GroupedDesc& g, const void* x, const void* w, void* y, bool mn, uint64_t timeout_ns,
+                         cudaStream_t s);
+size_t grouped_ws(int experts);
+// dW = alpha dy^T x + beta dW, dW of type `out` (ldw, w_stride).
+muon_status grouped_dw(const GroupedDesc& g, const void* dy, const void* x, void* dw, Op out, float alpha, float beta,
+                       void* ws, uint64_t timeout_ns, cudaStream_t s);
+
 // 2: tensor-core GEMMs use the CTA-pair kernel (default); 1: single-CTA kernel.
 void set_gemm_pair_mode(int pair);
 

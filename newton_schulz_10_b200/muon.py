@@ -31,7 +31,8 @@ EXPORTS = ("muon_set_wait_timeout_ns", "muon_set_gemm_cta_pair", "muon_status_st
            "muon_ns_workspace_size", "ns_polar", "gram_ns_polar", "normuon_scale", "muon_select_workspace_size",
            "select_rows", "muon_workspace_size", "muon_step", "muon_step_profiled", "muon_kernel_launch_count",
            "select_rows_noalloc", "muon_step_events", "muon_set_gemm_chain", "muon_momentum",
-           "muon_orthogonalize", "muon_apply_update")
+           "muon_orthogonalize", "muon_apply_update", "grouped_matmul", "grouped_matmul_dx", "grouped_matmul_dw",
+           "grouped_workspace_size")
 
 
 class NsParams(C.Structure):
@@ -59,6 +60,12 @@ class StepProfile(C.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class Grouped(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("experts", C.c_int32), ("tokens", C.c_int64), ("n", C.c_int64), ("k", C.c_int64),
+                ("ldx", C.c_int64), ("ldy", C.c_int64), ("ldw", C.c_int64), ("w_stride", C.c_int64),
+                ("offsets", C.c_void_p), ("dev_status", C.c_void_p)]
 
 
 class MuonError(RuntimeError):
@@ -121,6 +128,14 @@ def lib() -> C.CDLL:
         L.muon_apply_update.argtypes = [C.POINTER(Matrix), i32, C.POINTER(Params), C.POINTER(vp), C.POINTER(vp),
                                         C.POINTER(vp), vp]
         L.muon_apply_update.restype = i32
+        for name in ("grouped_matmul", "grouped_matmul_dx"):
+            fn = getattr(L, name)
+            fn.argtypes = [C.POINTER(Grouped), vp, vp, vp, vp]
+            fn.restype = i32
+        L.grouped_matmul_dw.argtypes = [C.POINTER(Grouped), vp, vp, vp, i32, f32, f32, vp, sz, vp]
+        L.grouped_matmul_dw.restype = i32
+        L.grouped_workspace_size.argtypes = [i32]
+        L.grouped_workspace_size.restype = sz
         L.muon_kernel_launch_count.argtypes = []
         L.muon_kernel_launch_count.restype = i64
         _lib = L
@@ -399,3 +414,117 @@ def muon_step(mats, p: Params | None = None, ws=None, stream=None) -> Step:
     s = Step(list(mats), p or step_params(), ws)
     s(stream)
     return s
+
+
+# ---------------------------------------------------------------------------
+# products grouped by expert
+# ---------------------------------------------------------------------------
+
+
+def _need(ok: bool, code: int, where: str) -> None:
+    if not ok:
+        raise MuonError(code, where)
+
+
+def _code_of(t, where: str) -> int:
+    import torch
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    _need(code is not None, ERR_DTYPE, where)
+    return code
+
+
+def _call_stream(t, stream):
+    """The CUDA device of t and the stream of the call: the given one, else
+    the current stream of that device (whatever device is current)."""
+    import torch
+    return torch.cuda.device(t.device), _stream(torch.cuda.current_stream(t.device) if stream is None else stream)
+
+
+def _row_stride(t, where: str) -> int:
+    """Row stride of a matrix (or of each matrix of a stack) with unit column stride."""
+    _need(t.shape[-1] == 1 or t.stride(-1) == 1, ERR_SHAPE, where)
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+
+
+def _grouped(where, x, y, w, offsets, dev_status):
+    """The descriptor of a call: x (tokens, k), y (tokens, n), w (experts, n, k)."""
+    import torch
+    _need(x.dim() == 2 and y.dim() == 2 and w.dim() == 3 and offsets.dim() == 1, ERR_SHAPE, where)
+    experts, n, k = w.shape
+    _need(x.shape[1] == k and y.shape == (x.shape[0], n) and offsets.shape[0] == experts + 1, ERR_SHAPE, where)
+    _need(x.dtype == y.dtype and x.dtype in (torch.bfloat16, torch.float16) and offsets.dtype == torch.int32, ERR_DTYPE, where)
+    _need(all(t.is_cuda and t.device == x.device for t in (x, y, w, offsets)) and offsets.is_contiguous(), ERR_INVALID_ARG, where)
+    if dev_status is not None:
+        _need(dev_status.dtype == torch.int32 and dev_status.device == x.device, ERR_INVALID_ARG, where)
+
+    def ld(t):
+        # the stride of a single row is never used: any aligned value will do
+        return _row_stride(t, where) if t.shape[-2] > 1 else -(-t.shape[-1] // 8) * 8
+
+    return Grouped(_code_of(x, where), experts, x.shape[0], n, k, ld(x), ld(y), ld(w), w.stride(0) if experts > 1 else 0,
+                   _ptr(offsets), _ptr(dev_status))
+
+
+def _grouped_out(out, shape, like):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    return out
+
+
+def grouped_matmul(x, w, offsets, out=None, dev_status=None, stream=None):
+    """y[r] = x[r] @ w[e].T for the rows r of every expert e.
+
+    x (tokens, k) holds the rows sorted by expert, w (experts, n, k) the
+    weights (bf16 or fp16, unit column stride, 16-byte rows), offsets
+    (experts + 1, int32, on the device) each expert's first row. Rows of `out`
+    (tokens, n) that belong to no expert keep their values."""
+    where = "grouped_matmul"
+    _need(x.dim() == 2 and w.dim() == 3, ERR_SHAPE, where)
+    y = _grouped_out(out, (x.shape[0], w.shape[1]), x)
+    _need(w.dtype == x.dtype, ERR_DTYPE, where)
+    g = _grouped(where, x, y, w, offsets, dev_status)
+    dev, s = _call_stream(x, stream)
+    with dev:
+        _check(lib().grouped_matmul(C.byref(g), _ptr(x), _ptr(w), _ptr(y), s), where)
+    return y
+
+
+def grouped_matmul_dx(dy, w, offsets, out=None, dev_status=None, stream=None):
+    """dx[r] = dy[r] @ w[e]: the gradient of grouped_matmul for its rows."""
+    where = "grouped_matmul_dx"
+    _need(dy.dim() == 2 and w.dim() == 3, ERR_SHAPE, where)
+    dx = _grouped_out(out, (dy.shape[0], w.shape[2]), dy)
+    _need(w.dtype == dy.dtype, ERR_DTYPE, where)
+    g = _grouped(where, dx, dy, w, offsets, dev_status)
+    dev, s = _call_stream(dy, stream)
+    with dev:
+        _check(lib().grouped_matmul_dx(C.byref(g), _ptr(dy), _ptr(w), _ptr(dx), s), where)
+    return dx
+
+
+def grouped_workspace_size(experts: int) -> int:
+    return lib().grouped_workspace_size(experts)
+
+
+def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float = 0.0, ws=None, dev_status=None, stream=None):
+    """out[e] = alpha * dy_e.T @ x_e + beta * out[e] over the rows of expert e:
+    the gradient of grouped_matmul for its weights (experts, n, k), in fp32 or
+    the type of dy and x. beta = 0 does not read `out`; without `out` the
+    result is fp32. With beta = the momentum decay and an fp32 momentum as
+    `out` this is M <- mu M + G without a gradient in memory."""
+    import torch
+    where = "grouped_matmul_dw"
+    _need(dy.dim() == 2 and x.dim() == 2 and offsets.dim() == 1 and offsets.shape[0] >= 1, ERR_SHAPE, where)
+    experts = offsets.shape[0] - 1
+    if out is None:
+        _need(beta == 0.0, ERR_INVALID_ARG, where)
+        out = torch.empty((experts, dy.shape[1], -(-x.shape[1] // 8) * 8), dtype=torch.float32, device=x.device)[:, :, :x.shape[1]]
+    g = _grouped(where, x, dy, out, offsets, dev_status)
+    if ws is None:
+        ws = workspace(grouped_workspace_size(experts), x.device)
+    dev, s = _call_stream(x, stream)
+    with dev:
+        _check(lib().grouped_matmul_dw(C.byref(g), _ptr(dy), _ptr(x), _ptr(out), _code_of(out, where), alpha, beta, _ptr(ws),
+                                       ws.numel(), s), where)
+    return out

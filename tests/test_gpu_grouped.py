@@ -1,0 +1,293 @@
+"""Products grouped by expert against the definition in 64 bits.
+
+Tolerances, per element, from the arithmetic: a product's terms are summed in
+fp32 in k / 16 instructions, each adding at most 2^-23 of the running sum of
+magnitudes (and a few times that inside the instruction), so the sum is off by
+at most (k / 16 + 8) 2^-23 sum |x| |w|; the result is rounded once to its
+type, half a step eps / 2 of its value (fp16: plus half a step 2^-25 of its
+subnormals). alpha and beta add two fp32 roundings.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from newton_schulz_10_b200 import muon as mu
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def offsets_of(counts, first=0):
+    return torch.tensor(np.cumsum([first, *counts]), dtype=torch.int32, device="cuda")
+
+
+def padded(t, extra=8):
+    """The same values with rows that are `extra` (and up to a 16-byte step) wider in memory, NaN behind."""
+    width = (t.shape[-1] + extra + 7) // 8 * 8
+    wide = torch.full((*t.shape[:-1], width), float("nan"), dtype=t.dtype, device=t.device)
+    wide[..., :t.shape[-1]] = t
+    return wide[..., :t.shape[-1]]
+
+
+def draw(shape, std, dtype, seed, pad=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = torch.randn(shape, generator=g, device="cuda") * std
+    t = t.to(dtype)
+    return padded(t) if pad or shape[-1] % 8 else t
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def close(got, want, magnitude, terms, dtype):
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    tol = half_step(dtype) * want.abs() + (1 + half_step(dtype)) * (terms / 16 + 8) * 2.0 ** -23 * magnitude + tiny
+    off = (got.double() - want).abs()
+    worst = (off / tol.clamp_min(1e-300)).max().item() if off.numel() else 0.0
+    assert bool((off <= tol).all()), f"{worst:.3g} times the tolerance"
+
+
+def rows_ref(x, w, off, transpose):
+    """(rows, product, sum of magnitudes) per expert"""
+    o = off.tolist()
+    for e in range(len(o) - 1):
+        r = slice(o[e], o[e + 1])
+        W = w[e].double()
+        W = W.T if transpose else W
+        yield r, x[r].double() @ W, x[r].double().abs() @ W.abs()
+
+
+COUNTS = {
+    "one_token": [1],
+    "decode": [1, 0, 1, 2, 0, 0, 1, 3],
+    "tiles": [31, 32, 33, 0, 64, 65, 1],
+    "wide": [255, 256, 257, 0, 513, 1],
+    "skewed": [0, 0, 1100, 3, 0, 17, 0],
+    "long": [1300, 700],
+}
+SIZES = {"small": (64, 64), "ragged": (200, 136), "odd": (77, 91), "narrow": (5, 3), "wide": (640, 1032)}
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("counts", list(COUNTS))
+def test_rows_products(cuda, counts, size, dtype):
+    n, k = SIZES[size]
+    c = COUNTS[counts]
+    d = DT[dtype]
+    off = offsets_of(c, first=3)
+    total = 3 + sum(c) + 5
+    x, w, dy = draw((total, k), 1.0, d, 1), draw((len(c), n, k), 0.1, d, 2), draw((total, n), 1.0, d, 3)
+    # rows of no expert hold NaN: none of it may reach a result
+    x[:3], x[total - 5:], dy[:3], dy[total - 5:] = (float("nan"),) * 4
+    y = draw((total, n), 1.0, d, 4)
+    dx = draw((total, k), 1.0, d, 5)
+    y0, dx0 = y.clone(), dx.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert mu.grouped_matmul(x, w, off, out=y, dev_status=status) is y
+    assert mu.grouped_matmul_dx(dy, w, off, out=dx, dev_status=status) is dx
+    for r, want, mag in rows_ref(x, w, off, True):
+        close(y[r], want, mag, k, d)
+    for r, want, mag in rows_ref(dy, w, off, False):
+        close(dx[r], want, mag, n, d)
+    for out, before in ((y, y0), (dx, dx0)):
+        assert torch.equal(out[:3], before[:3]) and torch.equal(out[total - 5:], before[total - 5:])
+    assert int(status.item()) == mu.OK
+
+
+def dw_ref(dy, x, off, alpha, beta, old):
+    o = off.tolist()
+    want, mag = [], []
+    for e in range(len(o) - 1):
+        r = slice(o[e], o[e + 1])
+        want.append(alpha * (dy[r].double().T @ x[r].double()))
+        mag.append(abs(alpha) * (dy[r].double().abs().T @ x[r].double().abs()))
+    want, mag = torch.stack(want), torch.stack(mag)
+    if beta:
+        want = want + beta * old.double()
+    return want, mag
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f16", "f32"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("alpha,beta", [(1.0, 0.0), (0.5, 0.95)])
+def test_weight_gradient(cuda, counts, size, dtype, out, alpha, beta):
+    n, k = SIZES[size]
+    c = COUNTS[counts]
+    d = DT[dtype]
+    o = torch.float32 if out == "f32" else d
+    off = offsets_of(c, first=3)
+    total = 3 + sum(c) + 5
+    x, dy = draw((total, k), 1.0, d, 6), draw((total, n), 1.0, d, 7)
+    x[:3], x[total - 5:], dy[:3], dy[total - 5:] = (float("nan"),) * 4
+    dw = draw((len(c), n, k), 1.0, o, 8)
+    old = dw.clone()
+    if beta == 0.0:
+        dw.fill_(float("nan"))  # not read
+    wide = dw._base if dw._base is not None else None
+    mu.grouped_matmul_dw(dy, x, off, out=dw, alpha=alpha, beta=beta)
+    want, mag = dw_ref(dy, x, off, alpha, beta, old)
+    tol = half_step(o) * want.abs() + 2.0 ** -22 * (want.abs() + abs(beta) * old.double().abs())
+    tol += 1.01 * (max(c) / 16 + 8) * 2.0 ** -23 * mag + (2.0 ** -25 if o == torch.float16 else 0.0)
+    off_by = (dw.double() - want).abs()
+    assert bool((off_by <= tol).all()), (off_by / tol.clamp_min(1e-300)).max().item()
+    if wide is not None:
+        assert bool(wide[..., k:].isnan().all())  # nothing behind the rows is written
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_neighbours_do_not_mix(cuda, dtype):
+    """NaN and infinities of one expert stay in its own rows and its own gradient."""
+    d = DT[dtype]
+    c = [37, 50, 70]
+    off = offsets_of(c)
+    x, w, dy = draw((157, 72), 1.0, d, 1), draw((3, 80, 72), 1.0, d, 2), draw((157, 80), 1.0, d, 3)
+    y, dx = mu.grouped_matmul(x, w, off), mu.grouped_matmul_dx(dy, w, off)
+    dw = mu.grouped_matmul_dw(dy, x, off)
+    x[37], x[86], dy[50], w[1, 3] = float("nan"), float("inf"), float("-inf"), float("nan")
+    y2, dx2 = mu.grouped_matmul(x, w, off), mu.grouped_matmul_dx(dy, w, off)
+    dw2 = mu.grouped_matmul_dw(dy, x, off)
+    keep = torch.cat([torch.arange(37), torch.arange(87, 157)]).cuda()
+    assert torch.equal(y2[keep], y[keep]) and torch.equal(dx2[keep], dx[keep])
+    assert torch.equal(dw2[[0, 2]], dw[[0, 2]])
+    assert bool(y2[37].isnan().all()) and bool(y2[38, 3].isnan()) and not bool(y2[38, :3].isnan().any())
+
+
+@pytest.mark.parametrize("experts,tokens", [(1024, 5000), (1000, 40), (2, 0), (1, 4097)])
+def test_many_and_few_experts(cuda, experts, tokens):
+    g = torch.Generator().manual_seed(experts)
+    c = torch.bincount(torch.randint(0, experts, (tokens,), generator=g), minlength=experts).tolist()
+    off = offsets_of(c)
+    d = torch.bfloat16
+    x, w, dy = draw((tokens, 40), 1.0, d, 1), draw((experts, 24, 40), 1.0, d, 2), draw((tokens, 24), 1.0, d, 3)
+    y, dx, dw = mu.grouped_matmul(x, w, off), mu.grouped_matmul_dx(dy, w, off), mu.grouped_matmul_dw(dy, x, off)
+    e = torch.repeat_interleave(torch.arange(experts), torch.tensor(c, dtype=torch.int64)).cuda()
+    want = torch.einsum("tk,tnk->tn", x.double(), w.double()[e])
+    close(y, want, torch.einsum("tk,tnk->tn", x.double().abs(), w.double()[e].abs()), 40, d)
+    want = torch.einsum("tn,tnk->tk", dy.double(), w.double()[e])
+    close(dx, want, torch.einsum("tn,tnk->tk", dy.double().abs(), w.double()[e].abs()), 24, d)
+    outer = dy.double()[:, :, None] * x.double()[:, None, :]
+    want = torch.zeros(experts, 24, 40, dtype=torch.float64, device="cuda").index_add_(0, e, outer)
+    mag = torch.zeros_like(want).index_add_(0, e, outer.abs())
+    assert bool(((dw.double() - want).abs() <= 2.0 ** -24 * want.abs() + (max(c) / 16 + 8) * 2.0 ** -23 * mag).all())
+
+
+def test_views_of_larger_tensors(cuda):
+    """Column blocks of x and y, row blocks of a fused weight (gate and up), a slice of the experts."""
+    d = torch.bfloat16
+    c = [70, 0, 33]
+    off = offsets_of(c)
+    X, Y = draw((103, 256), 1.0, d, 1), draw((103, 320), 1.0, d, 2)
+    W = draw((5, 2 * 96, 128), 0.1, d, 3)
+    x, y, up = X[:, 64:192], Y[:, 160:256], W[1:4, 96:]
+    before = Y.clone()
+    mu.grouped_matmul(x, up, off, out=y)
+    for r, want, mag in rows_ref(x, up, off, True):
+        close(y[r], want, mag, 128, d)
+    assert torch.equal(Y[:, :160], before[:, :160]) and torch.equal(Y[:, 256:], before[:, 256:])
+    G = torch.zeros((5, 2 * 96, 128), dtype=torch.float32, device="cuda")
+    mu.grouped_matmul_dw(y, x, off, out=G[1:4, 96:])
+    want, mag = dw_ref(y, x, off, 1.0, 0.0, None)
+    assert bool(((G[1:4, 96:].double() - want).abs() <= 2.0 ** -24 * want.abs() + 20 * 2.0 ** -23 * mag).all())
+    G[1:4, 96:] = 0
+    assert not bool(G.any())
+
+
+def test_graph_replay_reads_new_offsets(cuda):
+    d = torch.bfloat16
+    x, w, dy = draw((300, 128), 1.0, d, 1), draw((4, 96, 128), 0.1, d, 2), draw((300, 96), 1.0, d, 3)
+    off = offsets_of([100, 100, 50, 50])
+    y, dx = torch.zeros((300, 96), dtype=d, device="cuda"), torch.zeros((300, 128), dtype=d, device="cuda")
+    dw, ws = torch.zeros((4, 96, 128), device="cuda"), mu.workspace(mu.grouped_workspace_size(4))
+
+    def calls():
+        mu.grouped_matmul(x, w, off, out=y)
+        mu.grouped_matmul_dx(dy, w, off, out=dx)
+        mu.grouped_matmul_dw(dy, x, off, out=dw, ws=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for counts in ([100, 100, 50, 50], [0, 7, 260, 1], [300, 0, 0, 0], [0, 0, 0, 0]):
+        off.copy_(offsets_of(counts))
+        for t in (y, dx, dw):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, dx, dw)]
+        for t in (y, dx, dw):
+            t.zero_()
+        calls()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (y, dx, dw)):
+            assert torch.equal(a, b)
+        r = sum(counts)
+        assert not bool(y[r:].any()) and not bool(dx[r:].any())
+
+
+def test_on_another_stream_and_repeated(cuda):
+    """A call on a stream of its own sees what that stream wrote; the same call twice gives the same bits."""
+    d = torch.float16
+    x, w, off = draw((500, 264), 1.0, d, 1), draw((6, 320, 264), 0.1, d, 2), offsets_of([90, 0, 200, 10, 150, 50])
+    want = mu.grouped_matmul(x, w, off)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    x2 = torch.zeros_like(x)
+    with torch.cuda.stream(s):
+        x2.copy_(x)
+        got = mu.grouped_matmul(x2, w, off)
+    s.synchronize()
+    assert torch.equal(got, want) and torch.equal(mu.grouped_matmul(x, w, off), want)
+
+
+@pytest.mark.parametrize("bad", [[0, 30, 20, 40], [0, 10, 20, 41], [-1, 10, 20, 30], [0, 10, 2 ** 31 - 1, 40], [40, 30, 20, 10]])
+def test_bad_offsets_are_reported(cuda, bad):
+    """Entries out of range or decreasing: an error in the status word, nothing outside the matrices touched."""
+    d = torch.bfloat16
+    X, Y = draw((60, 64), 1.0, d, 1), draw((60, 64), 1.0, d, 2)
+    w = draw((3, 64, 64), 0.1, d, 3)
+    x, y = X[10:50], Y[10:50]
+    before = Y.clone()
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    for call in (lambda s: mu.grouped_matmul(x, w, off, out=y, dev_status=s), lambda s: mu.grouped_matmul_dx(x, w, off, out=y, dev_status=s),
+                 lambda s: mu.grouped_matmul_dw(x, x, off, dev_status=s)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(status)
+        assert int(status.item()) == mu.ERR_INVALID_ARG
+    assert torch.equal(Y[:10], before[:10]) and torch.equal(Y[50:], before[50:])
+
+
+def test_gradients_against_differences(cuda):
+    """loss = sum(y * c): its differences along random directions of x and W are the products with dx and dW.
+    The loss is linear in each, so a central difference has no error but the roundings of y (bf16, half a step of
+    each of its values, random: 2^-8 sqrt(sum (c y)^2) a side would be large against a small step; the step is as
+    large as the inputs) and of dx."""
+    d = torch.float16
+    c = [40, 0, 21]
+    off = offsets_of(c)
+    x, w, cot = draw((61, 96), 1.0, d, 1), draw((3, 80, 96), 0.1, d, 2), draw((61, 80), 1.0, d, 3)
+    dx, dw = mu.grouped_matmul_dx(cot, w, off), mu.grouped_matmul_dw(cot, x, off)
+    ux, uw = draw((61, 96), 1.0, d, 4), draw((3, 80, 96), 0.1, d, 5)
+
+    def loss(x_, w_):
+        return (mu.grouped_matmul(x_, w_, off).double() * cot.double()).sum().item()
+
+    # exact in fp16: x +- u halves are rounded, so differentiate along the rounded points
+    for a, b, grad in (((x + ux, w), (x - ux, w), dx), ((x, w + uw), (x, w - uw), dw)):
+        delta = (a[0].double() - b[0].double(), a[1].double() - b[1].double())
+        slope = (grad.double() * (delta[0] if grad is dx else delta[1])).sum().item()
+        ya, yb = mu.grouped_matmul(*a, off).double(), mu.grouped_matmul(*b, off).double()
+        # half a step of every y and of every dx, all of one sign at worst
+        tol = 2.0 ** -11 * ((ya.abs() + yb.abs()) * cot.double().abs()).sum().item()
+        if grad is dx:
+            tol += 2.0 ** -11 * (dx.double().abs() * delta[0].abs()).sum().item()
+        assert abs(loss(*a) - loss(*b) - slope) <= 1.01 * tol
