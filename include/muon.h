@@ -53,7 +53,11 @@ typedef enum {
   MUON_ERR_UNSUPPORTED = 9   /* valid request this build cannot serve         */
 } muon_status;
 
-typedef enum { MUON_F32 = 0, MUON_BF16 = 1, MUON_F16 = 2 } muon_dtype;
+/* MUON_F16X2 is no element type of memory: as muon_ns_params.compute of
+ * muon_stack_step it keeps every operand of the chain as the sum of two fp16
+ * planes (22 bits), about fp32 accuracy on the tensor cores. The other entry
+ * points answer it with MUON_ERR_DTYPE. */
+typedef enum { MUON_F32 = 0, MUON_BF16 = 1, MUON_F16 = 2, MUON_F16X2 = 3 } muon_dtype;
 
 /* Dion3 row-selection key: the page's rule is the l1 norm of each momentum
  * row ("3. Dion3 Update Rule", Algorithm 4, step 1); l2 is an option. */
@@ -396,6 +400,77 @@ size_t grouped_workspace_size(int32_t experts);
  * is the first line of Eq. (1), M <- mu M + G, without a gradient in memory. */
 muon_status grouped_matmul_dw(const muon_grouped* g, const void* dy, const void* x, void* dw, muon_dtype dw_dtype,
                               float alpha, float beta, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- The update of stacks of matrices ------------------------------------
+ *
+ * A stack is `count` matrices of rows x cols at regular strides: the experts
+ * of a layer, the heads or the gate and up blocks of a fused projection, one
+ * padded matrix. Matrix b, row r of W starts at W + b w_stride + r w_ld
+ * (elements), the others alike; columns are adjacent.
+ *   W      F32, BF16 or F16, updated in place
+ *   M      fp32 momentum, updated in place
+ *   G      gradient (F32, BF16 or F16), read only; NULL when M already holds
+ *          this step's gradient (grouped_matmul_dw with beta = mu)
+ *   copy   NULL, or a BF16 / F16 array that receives the new W rounded once
+ *          (the weights that 16-bit products read beside an fp32 W)
+ * Strides and pointers need only their elements' alignment (16-byte rows of
+ * every array, a multiple of 4 columns, run faster). The matrices of W, M and
+ * copy may not overlap: they follow one another (stride >= (rows-1) ld + cols)
+ * or lie side by side in wider rows (ld >= (count-1) stride + cols);
+ * MUON_ERR_SHAPE otherwise. G may repeat (strides of 0). w_ld and the others
+ * are not read for a single row, strides not for a single matrix. At most
+ * 65535 matrices a stack. */
+typedef struct {
+  void* W;
+  float* M;
+  const void* G;
+  void* copy;
+  muon_dtype w_dtype;
+  muon_dtype g_dtype;
+  muon_dtype copy_dtype;
+  int64_t count;
+  int64_t rows;
+  int64_t cols;
+  int64_t w_stride, w_ld;
+  int64_t m_stride, m_ld;
+  int64_t g_stride, g_ld;
+  int64_t copy_stride, copy_ld;
+} muon_stack;
+
+/*   mu, lr        momentum and learning rate
+ *   weight_decay  decoupled: W is first multiplied by 1 - lr weight_decay
+ *   scale         factor of the orthogonalised update, for example
+ *                 0.2 sqrt(max(rows, cols)) (entries of about 0.2)
+ *   nesterov      1: orthogonalise G + mu M (M already updated) instead of M;
+ *                 needs G
+ *   ns            compute may be MUON_F16X2 (gram = 0 only, else
+ *                 MUON_ERR_UNSUPPORTED)
+ *   dev_status    as in muon_params */
+typedef struct {
+  float mu;
+  float lr;
+  float weight_decay;
+  float scale;
+  int32_t nesterov;
+  muon_ns_params ns;
+  int32_t* dev_status;
+} muon_stack_params;
+
+/* mu = 0.95, lr = 0.02, no decay, scale = 1, no Nesterov, default ns. */
+void muon_stack_params_default(muon_stack_params* p);
+
+/* Workspace bytes of muon_stack_step (0 for invalid arguments); only shapes
+ * and p matter. Query with the device that will run the step current. */
+size_t muon_stack_workspace_size(const muon_stack* stacks, int32_t count, const muon_stack_params* p);
+
+/* One Muon update of every matrix of `count` stacks:
+ *   M <- mu M + G (when G is given);  X = M, or G + mu M with nesterov;
+ *   O = polar(X) by p->ns;  W <- (1 - lr weight_decay) W - lr scale O
+ * each rounded once. A matrix of zeros has the update 0 (an expert that never
+ * saw a token). Deferred errors as for muon_step: to p->dev_status, else to
+ * the first 4 workspace bytes. */
+muon_status muon_stack_step(const muon_stack* stacks, int32_t count, const muon_stack_params* p, void* ws, size_t ws_bytes,
+                            void* stream);
 
 /* Number of kernels this library has queued from the calling thread since it
  * was loaded (monotonic; for counting launches inside a timed region). */

@@ -7,6 +7,7 @@
 
 #include "internal.h"
 #include "rowops.cuh"
+#include "stack.cuh"
 
 namespace muon {
 
@@ -975,6 +976,244 @@ muon_status grouped_matmul_dw(const muon_grouped* g, const void* dy, const void*
   const GroupedDesc d = grouped_desc(g, t);
   if (!grouped_fits(d)) return MUON_ERR_SHAPE;
   return grouped_dw(d, dy, x, dw, ot, alpha, beta, ws, timeout_ns(), static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// the update of stacks of matrices
+// ---------------------------------------------------------------------------
+
+namespace {
+
+bool type_ok(muon_dtype d) { return d == MUON_F32 || d == MUON_BF16 || d == MUON_F16; }
+int64_t bytes_of(muon_dtype d) { return d == MUON_F32 ? 4 : 2; }
+
+// Strides of one array of a stack. apart: its matrices may not share elements.
+muon_status check_strides(const muon_stack& k, int64_t stride, int64_t ld, bool apart) {
+  if ((k.rows > 1 && ld < (apart ? k.cols : 0)) || (k.count > 1 && stride < 0)) return MUON_ERR_SHAPE;
+  if (apart && k.count > 1) {
+    const int64_t span = (k.rows - 1) * (k.rows > 1 ? ld : 0) + k.cols;  // one matrix after the other, or
+    const bool after = stride >= span;
+    // side by side within wider rows
+    const bool beside = stride >= k.cols && (k.rows == 1 || ld >= (k.count - 1) * stride + k.cols);
+    if (!after && !beside) return MUON_ERR_SHAPE;
+  }
+  return MUON_OK;
+}
+
+bool empty_stack(const muon_stack& k) { return k.count == 0 || k.rows == 0 || k.cols == 0; }
+
+// shapes_only: for the size query, which reads no pointer and no stride.
+muon_status check_stacks(const muon_stack* st, int32_t count, const muon_stack_params* p, bool shapes_only, Op* t,
+                         int* planes) {
+  if (!p || count < 0 || (count > 0 && !st)) return MUON_ERR_INVALID_ARG;
+  muon_ns_params ns = p->ns;
+  *planes = 1;
+  if (ns.compute == MUON_F16X2) {
+    *planes = 2;
+    ns.compute = MUON_F16;
+    if (ns.gram) return MUON_ERR_UNSUPPORTED;  // the Gram chain carries one plane
+  }
+  TRY(check_ns(&ns));
+  op_of(ns.compute, t);
+  if (!std::isfinite(p->mu) || !std::isfinite(p->lr) || !std::isfinite(p->weight_decay) || !std::isfinite(p->scale))
+    return MUON_ERR_INVALID_ARG;
+  if (p->nesterov != 0 && p->nesterov != 1) return MUON_ERR_INVALID_ARG;
+  if (p->dev_status && (reinterpret_cast<uintptr_t>(p->dev_status) & 3u)) return MUON_ERR_ALIGN;
+  int64_t rows = 0;
+  for (int i = 0; i < count; ++i) {
+    const muon_stack& k = st[i];
+    if (k.count < 0 || k.rows < 0 || k.cols < 0 || k.count > INT32_MAX || k.rows > INT32_MAX || k.cols > INT32_MAX - 256)
+      return MUON_ERR_SHAPE;
+    if (empty_stack(k)) continue;
+    if (k.count > INT32_MAX / k.rows || (rows += k.count * k.rows) > INT32_MAX / 2) return MUON_ERR_SHAPE;
+    if (k.count > 65535) return MUON_ERR_SHAPE;
+    if (shapes_only) continue;
+    if (!k.W || !k.M || (p->nesterov && !k.G)) return MUON_ERR_INVALID_ARG;
+    if (!type_ok(k.w_dtype) || (k.G && !type_ok(k.g_dtype)) ||
+        (k.copy && k.copy_dtype != MUON_BF16 && k.copy_dtype != MUON_F16))
+      return MUON_ERR_DTYPE;
+    auto odd = [](const void* ptr, int64_t es) { return reinterpret_cast<uintptr_t>(ptr) % (uintptr_t)es != 0; };
+    if (odd(k.W, bytes_of(k.w_dtype)) || odd(k.M, 4) || (k.G && odd(k.G, bytes_of(k.g_dtype))) || (k.copy && odd(k.copy, 2)))
+      return MUON_ERR_ALIGN;
+    TRY(check_strides(k, k.w_stride, k.w_ld, true));
+    TRY(check_strides(k, k.m_stride, k.m_ld, true));
+    if (k.G) TRY(check_strides(k, k.g_stride, k.g_ld, false));
+    if (k.copy) TRY(check_strides(k, k.copy_stride, k.copy_ld, true));
+  }
+  return MUON_OK;
+}
+
+struct StackPlan {
+  struct Grp {
+    int stack;
+    GroupBufs b;
+    size_t row_base, mat_base;
+  };
+  std::vector<Grp> groups;
+  size_t scale, xscale, rsum, ctr, total;
+};
+
+StackPlan plan_stacks(const muon_stack* st, int32_t count, const muon_ns_params* ns, Op t, int planes) {
+  StackPlan q;
+  size_t rows = 0, mats = 0;
+  for (int i = 0; i < count; ++i) {
+    if (empty_stack(st[i])) continue;
+    q.groups.push_back(StackPlan::Grp{i, {}, rows, mats});
+    rows += (size_t)st[i].count * st[i].rows;
+    mats += (size_t)st[i].count;
+  }
+  int64_t chain = 0;  // matrices of the largest chain, as in plan_step
+  for (size_t g0 = 0; g0 < q.groups.size(); g0 += kMaxGemmGroups) {
+    int64_t m = 0;
+    for (size_t g = g0; g < q.groups.size() && g < g0 + kMaxGemmGroups; ++g) m += st[q.groups[g].stack].count;
+    chain = m > chain ? m : chain;
+  }
+  size_t off = kAlign;  // status word
+  q.scale = off; off += up(mats * sizeof(float) + 4);
+  q.xscale = off; off += up(mats * sizeof(float) + 4);
+  q.rsum = off; off += up(rows * sizeof(double) + 8);
+  q.ctr = off; off += up(ns_counter_words(ns, chain) * sizeof(unsigned) + 4);
+  for (auto& g : q.groups) {
+    const muon_stack& k = st[g.stack];
+    if (planes == 2) {
+      // both planes of every matrix; no split of K, so no scratch
+      const int64_t n = k.rows < k.cols ? k.rows : k.cols;
+      const size_t xb = up((size_t)k.count * 2 * k.rows * pad_ld(k.cols) * 2), nb = up((size_t)k.count * 2 * n * pad_ld(n) * 2);
+      for (int i = 0; i < 2; ++i) {
+        g.b.X[i] = off; off += xb;
+        g.b.nb[i] = off; off += nb;
+      }
+      g.b.part = off;
+      g.b.part_bytes = 0;
+    } else {
+      off = layout_group(k.rows, k.cols, (int)k.count, t, ns, off, &g.b);
+    }
+  }
+  q.total = off;
+  return q;
+}
+
+// Storage scales of two-plane operands: powers of two (exact) that bring the
+// entries of X_0 (root mean square 1 / sqrt(rows cols)) and of the Gram
+// matrix (diagonal about 1 / n at first, 1 at the end) near 1, capped so that
+// neither the final X (entries up to 1) nor a polynomial of norm up to 16
+// leaves fp16's range.
+float pow2_near(double x, double most) {
+  double p = 1.0;
+  while (p * 1.5 < x && p < most) p *= 2.0;
+  return (float)p;
+}
+
+muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_params* p, void* ws, size_t ws_bytes,
+                       cudaStream_t s) {
+  Op t;
+  int planes;
+  TRY(check_stacks(st, count, p, false, &t, &planes));
+  muon_ns_params ns = p->ns;
+  if (planes == 2) ns.compute = MUON_F16;
+  const StackPlan q = plan_stacks(st, count, &ns, t, planes);
+  if (q.groups.empty()) return MUON_OK;
+  if (!ws) return MUON_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MUON_ERR_ALIGN;
+  if (ws_bytes < q.total) return MUON_ERR_WORKSPACE;
+  int* status = p->dev_status ? p->dev_status : at<int>(ws, 0);
+  if (!p->dev_status && cudaMemsetAsync(status, 0, sizeof(int), s) != cudaSuccess) return MUON_ERR_CUDA;
+
+  // bf16 operands are stored unscaled, in the momentum pass itself, and the
+  // Frobenius scale enters the first products; the others are scaled once
+  // the norm is known.
+  const bool folded = planes == 1 && t == Op::BF16;
+  std::vector<NsGroup> groups;
+  std::vector<StackLaunch> launches((q.groups.size() + kMaxStacks - 1) / kMaxStacks);
+  for (size_t gi = 0; gi < q.groups.size(); ++gi) {
+    const StackPlan::Grp& g = q.groups[gi];
+    const muon_stack& k = st[g.stack];
+    const int64_t n = k.rows < k.cols ? k.rows : k.cols, m = k.rows < k.cols ? k.cols : k.rows;
+    StackLaunch& L = launches[gi / kMaxStacks];
+    if (gi % kMaxStacks == 0) {
+      memset(&L, 0, sizeof(L));
+      L.rsum = at<double>(ws, q.rsum) + g.row_base;
+      L.scale = at<float>(ws, q.scale) + g.mat_base;
+      L.xscale = at<float>(ws, q.xscale) + g.mat_base;
+      L.mu = p->mu;
+      L.step = p->lr * p->scale;
+      L.keep = 1.f - p->lr * p->weight_decay;
+      L.eps = ns.norm_eps;
+      L.nesterov = p->nesterov;
+      L.folded = folded;
+      L.status = status;
+    }
+    StackMat& e = L.m[L.count++];
+    e.W = k.W; e.w_stride = k.w_stride; e.w_ld = k.w_ld; e.w_type = k.w_dtype;
+    e.M = k.M; e.m_stride = k.m_stride; e.m_ld = k.m_ld;
+    e.G = k.G; e.g_stride = k.g_stride; e.g_ld = k.g_ld; e.g_type = k.g_dtype;
+    e.copy = k.copy; e.c_stride = k.copy_stride; e.c_ld = k.copy_ld; e.c_type = k.copy_dtype;
+    e.X = at<void>(ws, g.b.X[0]);
+    e.ldx = pad_ld(k.cols);
+    e.rows = (int32_t)k.rows; e.cols = (int32_t)k.cols; e.count = (int32_t)k.count;
+    e.row_begin = L.total_rows;
+    e.mat_begin = L.total_mats;
+    L.total_rows += (int)(k.count * k.rows);
+    L.total_mats += (int)k.count;
+    e.kappa = planes == 2 ? pow2_near(std::sqrt((double)n * m), 16384.0) : folded ? 1.f : kappa_for(t, n);
+    auto four = [](const void* ptr, int64_t es, int64_t ld, int64_t stride) {
+      return !ptr || (reinterpret_cast<uintptr_t>(ptr) % (uintptr_t)(4 * es) == 0 && ld % 4 == 0 && stride % 4 == 0);
+    };
+    e.vec = k.cols % 4 == 0 && four(k.W, bytes_of(k.w_dtype), k.w_ld, k.w_stride) && four(k.M, 4, k.m_ld, k.m_stride) &&
+            four(k.G, k.G ? bytes_of(k.g_dtype) : 4, k.g_ld, k.g_stride) && four(k.copy, 2, k.copy_ld, k.copy_stride);
+
+    NsGroup ng{};
+    ng.rows = k.rows;
+    ng.cols = k.cols;
+    ng.count = (int)k.count;
+    ng.X[0] = at<void>(ws, g.b.X[0]);
+    ng.X[1] = at<void>(ws, g.b.X[1]);
+    ng.xscale = at<float>(ws, q.xscale) + g.mat_base;
+    for (int i = 0; i < (planes == 2 ? 2 : ns_work_buffers(&ns)); ++i) ng.nb[i] = at<void>(ws, g.b.nb[i]);
+    ng.rho = planes == 2 ? pow2_near((double)n, 4096.0) : rho_for(t, n);
+    ng.part = g.b.part_bytes ? at<float>(ws, g.b.part) : nullptr;
+    ng.part_bytes = g.b.part_bytes;
+    ng.planes = planes;
+    ng.kappa = e.kappa;
+    groups.push_back(ng);
+  }
+  for (StackLaunch& L : launches) {
+    TRY(launch_stack_momentum(L, t, folded, s));
+    TRY(launch_stack_norm(L, s));
+    if (!folded) TRY(launch_stack_cast(L, t, planes, s));
+  }
+  for (size_t g0 = 0; g0 < groups.size(); g0 += kMaxGemmGroups) {
+    const int ng = (int)(groups.size() - g0 < (size_t)kMaxGemmGroups ? groups.size() - g0 : kMaxGemmGroups);
+    TRY(ns_run(t, groups.data() + g0, ng, &ns, status, timeout_ns(), s, at<unsigned>(ws, q.ctr)));
+  }
+  for (size_t gi = 0; gi < groups.size(); ++gi) launches[gi / kMaxStacks].m[gi % kMaxStacks].X = groups[gi].X[groups[gi].cur];
+  for (const StackLaunch& L : launches) TRY(launch_stack_update(L, t, planes, s));
+  return MUON_OK;
+}
+
+}  // namespace
+
+void muon_stack_params_default(muon_stack_params* p) {
+  if (!p) return;
+  memset(p, 0, sizeof(*p));
+  p->mu = 0.95f;
+  p->lr = 0.02f;
+  p->scale = 1.f;
+  muon_ns_params_default(&p->ns);
+}
+
+size_t muon_stack_workspace_size(const muon_stack* stacks, int32_t count, const muon_stack_params* p) {
+  Op t;
+  int planes;
+  if (check_stacks(stacks, count, p, true, &t, &planes) != MUON_OK) return 0;
+  muon_ns_params ns = p->ns;
+  if (planes == 2) ns.compute = MUON_F16;
+  return plan_stacks(stacks, count, &ns, t, planes).total;
+}
+
+muon_status muon_stack_step(const muon_stack* stacks, int32_t count, const muon_stack_params* p, void* ws, size_t ws_bytes,
+                            void* stream) {
+  return stack_impl(stacks, count, p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int64_t muon_kernel_launch_count(void) { return counters().launches; }

@@ -41,6 +41,15 @@
 // deterministic and exactly symmetric) or, when not split, runs on
 // 128-column tiles if they all fit in one wave.
 //
+// Two planes (PL = 2, fp16): a matrix is the sum of two fp16 planes, hi =
+// fp16(x) and lo = fp16(x - hi), 22 bits of x, stored as matrices 2b and
+// 2b + 1 of its buffer. A stage holds both planes of both operands (one box
+// each), and every k-step issues three MMAs into the same fp32 accumulator,
+// hi hi + hi lo + lo hi (the dropped lo lo is 2^-22 of the product); the
+// epilogue adds both planes of C and splits the result again. Four loads feed
+// three MMAs, so a tile moves 2/3 of the bytes per MMA of the single-plane
+// form, with stages twice as large and half as many.
+//
 // Every wait is bounded (mbar_wait_bounded): on expiry the kernel records
 // MUON_ERR_TIMEOUT, every role stops (in both CTAs of a pair), in-flight
 // copies and MMAs are drained with bounded waits (for a pair, by counting
@@ -74,11 +83,11 @@ constexpr int EPI_BUF = 2 * EPI_BLOCK;             // per epilogue warp: direct 
 // a tiny configurable wait budget never lets a CTA exit with work in flight.
 constexpr uint64_t DRAIN_NS = 1000000000ull;
 
-template <int PAIR, int BN>
+template <int PAIR, int BN, int PL = 1>
 struct Cfg {
-  static constexpr int STAGES = PAIR == 2 ? (BN == BN_WIDE ? 6 : 8) : (BN == BN_WIDE ? 4 : 6);
-  static constexpr int A_STAGE = BM * BK * 2;                  // this CTA's 128 rows of A
-  static constexpr int B_STAGE = (BN / PAIR) * BK * 2;         // this CTA's share of B's BN rows
+  static constexpr int STAGES = (PAIR == 2 ? (BN == BN_WIDE ? 6 : 8) : (BN == BN_WIDE ? 4 : 6)) / PL;
+  static constexpr int A_STAGE = BM * BK * 2 * PL;             // this CTA's 128 rows of A (all planes)
+  static constexpr int B_STAGE = (BN / PAIR) * BK * 2 * PL;    // this CTA's share of B's BN rows
   static constexpr int EPI_CHUNKS = BN / 32 / 2;               // 32-column chunks per epilogue warp
   static constexpr int TX_BYTES = PAIR * (A_STAGE + B_STAGE);  // per stage, both CTAs
   static constexpr int TILE_M = BM * PAIR;                     // rows of a (pair) tile
@@ -284,9 +293,9 @@ __device__ __forceinline__ bool wait_dep(const Params& p, const Job& g, int b, v
 // For those, the barrier is settled for the copies that were never issued
 // (the missing transaction bytes, or the leader's arrival with the bytes that
 // were issued), then waited on with the drain bound.
-template <int PAIR, int BN>
+template <int PAIR, int BN, int PL>
 __device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
-  using Cf = Cfg<PAIR, BN>;
+  using Cf = Cfg<PAIR, BN, PL>;
   constexpr int STAGES = Cf::STAGES;
   const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
   const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
@@ -307,9 +316,10 @@ __device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int*
   }
 }
 
-template <typename T, int PAIR, int BN>
+template <typename T, int PAIR, int BN, int PL>
 __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant__ Params p) {
-  using Cf = Cfg<PAIR, BN>;
+  using Cf = Cfg<PAIR, BN, PL>;
+  static_assert(PL == 1 || std::is_same<T, __half>::value, "two planes are fp16");
   constexpr int EPI_CHUNKS = Cf::EPI_CHUNKS;
   constexpr int STAGES = Cf::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -430,22 +440,22 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         uint8_t* b = sB + stage * Cf::B_STAGE;
         const int k0 = kb * BK;
         auto load = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
-          if (PAIR == 2) tma_load_3d_pair(dst, m, c0, c1, t.b, &full[stage]);
-          else tma_load_3d(dst, m, c0, c1, t.b, &full[stage]);
+          if (PAIR == 2) tma_load_3d_pair(dst, m, c0, c1, t.b * PL, &full[stage]);
+          else tma_load_3d(dst, m, c0, c1, t.b * PL, &full[stage]);
         };
         if (issues_a) {
           if (!g.a_mn) {
             load(a, mapA, k0, am0);
           } else {
             load(a, mapA, am0, k0);
-            load(a + 8192, mapA, am0 + 64, k0);
+            load(a + 8192 * PL, mapA, am0 + 64, k0);
           }
         } else {
           if (!g.b_mn) {
             load(b, mapB, k0, bn0);
           } else {
 #pragma unroll
-            for (int j = 0; j < BN / PAIR / 64; ++j) load(b + j * 8192, mapB, bn0 + 64 * j, k0);
+            for (int j = 0; j < BN / PAIR / 64; ++j) load(b + j * 8192 * PL, mapB, bn0 + 64 * j, k0);
           }
         }
         ++issued;
@@ -492,7 +502,13 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
       // K-major: 8-row groups 1024 B apart, one K step = 32 B inside the
       // swizzle atom. MN-major: 64-element MN atoms 8 KB apart (LBO), 8-row
       // K groups 1024 B apart (SBO), one K step of 16 rows = 2048 B.
-      const uint32_t a_lbo = g.a_mn ? 8192u : 16u, b_lbo = g.b_mn ? 8192u : 16u;
+      // Two planes: an MN-major box holds 64 elements of both planes, so the
+      // atoms are 16 KB apart and the low plane 8 KB behind; K-major planes
+      // follow one another.
+      const uint32_t a_lbo = g.a_mn ? 8192u * PL : 16u, b_lbo = g.b_mn ? 8192u * PL : 16u;
+      const uint32_t a_low = (g.a_mn ? 8192u : Cf::A_STAGE / 2u) >> 4, b_low = (g.b_mn ? 8192u : Cf::B_STAGE / 2u) >> 4;
+      (void)a_low;
+      (void)b_low;
       const uint32_t a_kstep = g.a_mn ? 2048u : 32u, b_kstep = g.b_mn ? 2048u : 32u;
       // descriptor fields other than the start address, fixed for the tile;
       // start addresses (>> 4) stay below 2^14 inside the 228 KB window
@@ -520,6 +536,15 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
           const bool accumulate = kb != t.kb0 || k != 0;
           if (PAIR == 2) umma_f16_pair(d_tmem, ad, bd, idesc, accumulate);
           else umma_f16(d_tmem, ad, bd, idesc, accumulate);
+          if (PL == 2) {
+            if (PAIR == 2) {
+              umma_f16_pair(d_tmem, ad, bd + b_low, idesc, true);
+              umma_f16_pair(d_tmem, ad + a_low, bd, idesc, true);
+            } else {
+              umma_f16(d_tmem, ad, bd + b_low, idesc, true);
+              umma_f16(d_tmem, ad + a_low, bd, idesc, true);
+            }
+          }
         }
         // frees the stage (in both CTAs) once these MMAs have read it
         if (PAIR == 2) umma_commit_pair(&empty[stage], 0x3); else umma_commit(&empty[stage]);
@@ -586,7 +611,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
       // wait. Loads are coalesced: load j of a chunk covers block rows
       // 8j..8j+7, four lanes per 64-byte row; the block is staged in shared
       // memory later and read back in the fragment layout with ldmatrix.
-      uint4 cv[EPI_CHUNKS][4];
+      // Two planes: only the next chunk's two blocks are held (cv[0], cv[1]),
+      // the following chunk's are loaded once these are staged.
+      constexpr int CV = PL == 1 ? EPI_CHUNKS : PL;
+      uint4 cv[CV][4];
       const bool part = g.splits > 1;  // store the raw fp32 partial accumulator
       const bool want_c = g.beta != 0.f && !part;  // warp-uniform
       if (want_c && g.dep >= 0) {
@@ -608,19 +636,26 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
           break;
         }
       }
-      if (want_c) {
-        const T* cb = reinterpret_cast<const T*>(g.C) + (long long)t.b * g.sC + (lane & 3) * 8;
+      // C block of one 32-column chunk (and plane) into cv[slot]
+      auto load_c = [&](int ch, int plane, int slot) {
+        const T* cb = reinterpret_cast<const T*>(g.C) + ((long long)t.b * PL + plane) * g.sC + (lane & 3) * 8;
+        const int c0 = cbase + ch * 32;
+        if (c0 < g.N && !(g.sym && c0 > r0 + 31)) {
 #pragma unroll
-        for (int ch = 0; ch < EPI_CHUNKS; ++ch) {
-          const int c0 = cbase + ch * 32;
-          if (c0 < g.N && !(g.sym && c0 > r0 + 31)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int cr = r0 + 8 * j + (lane >> 2);
-              if (cr < g.M && MUON_IN_BOUNDS(c0 + (lane & 3) * 8 + 8 <= g.ldc, p.status))
-                cv[ch][j] = __ldcg(reinterpret_cast<const uint4*>(cb + (long long)cr * g.ldc + c0));
-            }
+          for (int j = 0; j < 4; ++j) {
+            const int cr = r0 + 8 * j + (lane >> 2);
+            if (cr < g.M && MUON_IN_BOUNDS(c0 + (lane & 3) * 8 + 8 <= g.ldc, p.status))
+              cv[slot][j] = __ldcg(reinterpret_cast<const uint4*>(cb + (long long)cr * g.ldc + c0));
           }
+        }
+      };
+      if (want_c) {
+        if (PL == 1) {
+#pragma unroll
+          for (int ch = 0; ch < EPI_CHUNKS; ++ch) load_c(ch, 0, ch);
+        } else {
+#pragma unroll
+          for (int pl = 0; pl < PL; ++pl) load_c(0, pl, pl);
         }
       }
       // every lane waits; the result is made warp-uniform so the warp-wide
@@ -683,21 +718,29 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
           // C block through the mirror staging block (64-byte swizzle):
           // written as loaded, read back in the fragment layout
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(sm + sw64(8 * j + (lane >> 2), (lane & 3) * 8)) = cv[ch][j];
-          __syncwarp();
+          for (int pl = 0; pl < PL; ++pl) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // k = 2h + s
-            uint32_t cf[4];
-            ldsm_x4(sm_a + sw64(16 * (k >> 1) + 8 * (k & 1) + (lane & 7), 8 * (lane >> 3)), cf);
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(sm + sw64(8 * j + (lane >> 2), (lane & 3) * 8)) = cv[PL == 1 ? ch : pl][j];
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = Elem<T>::unpack2(cf[i]);
-              const int x = 16 * (k >> 1) + 4 * i + 2 * (k & 1);
-              v[x] += beta * f.x;
-              v[x + 1] += beta * f.y;
+            for (int k = 0; k < 4; ++k) {  // k = 2h + s
+              uint32_t cf[4];
+              ldsm_x4(sm_a + sw64(16 * (k >> 1) + 8 * (k & 1) + (lane & 7), 8 * (lane >> 3)), cf);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = Elem<T>::unpack2(cf[i]);
+                const int x = 16 * (k >> 1) + 4 * i + 2 * (k & 1);
+                v[x] += beta * f.x;
+                v[x + 1] += beta * f.y;
+              }
             }
+            __syncwarp();  // the C block is read before the staging block is overwritten
           }
-          __syncwarp();  // the C block is read before the staging block is overwritten
+          if (PL == 2 && ch + 1 < EPI_CHUNKS) {
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) load_c(ch + 1, pl, pl);
+          }
         }
         if (g.gamma != 0.f) {
 #pragma unroll
@@ -707,45 +750,58 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             if (r0 + rr == c0 + cc) v[x] += g.gamma;
           }
         }
-        // Round once to the stored type: the direct and mirrored copies of an
-        // element are the same bits, so D is exactly symmetric.
-        uint32_t pk[16];  // pk[4k + i]: matrix (h, s, i) with k = 2h + s
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int x = 16 * (k >> 1) + 4 * i + 2 * (k & 1);
-            pk[4 * k + i] = Elem<T>::pack2(v[x], v[x + 1]);
-          }
         const bool diag = g.sym && c0 == r0;   // the block straddles the diagonal
         const bool mirror = g.sym && r0 > c0;  // strictly lower: also store its transpose
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          stsm_x4(sd_a + sw64(16 * (k >> 1) + 8 * (k & 1) + (lane & 7), 8 * (lane >> 3)), pk[4 * k], pk[4 * k + 1],
-                  pk[4 * k + 2], pk[4 * k + 3]);
-        if (diag || mirror) {
-          // the transposed block: matrix (h, s, i) lands at rows 8i.., columns 16h + 8s..
+        for (int pl = 0; pl < PL; ++pl) {
+          // Round once to the stored type: the direct and mirrored copies of an
+          // element are the same bits, so D is exactly symmetric. With two
+          // planes the second holds what the first rounded away.
+          uint32_t pk[16];  // pk[4k + i]: matrix (h, s, i) with k = 2h + s
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            stsm_x4_trans(sm_a + sw64(lane, 16 * (k >> 1) + 8 * (k & 1)), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2],
-                          pk[4 * k + 3]);
-        }
-        if (diag) {
-          // symmetrise the diagonal block: above the diagonal (row < col)
-          // takes the value computed below it, from the transposed block
-          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j > lane)
-              *reinterpret_cast<uint16_t*>(sd + sw64(lane, j)) = *reinterpret_cast<const uint16_t*>(sm + sw64(lane, j));
-        }
-        fence_async_smem();  // generic-proxy writes become visible to the bulk copy
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&p.maps[g.mD], smem_u32(sd), c0, r0, t.b);
-          if (mirror) tma_store_3d(&p.maps[g.mD], smem_u32(sm), r0, c0, t.b);
-          bulk_commit();
-          ++groups;
+            for (int i = 0; i < 4; ++i) {
+              const int x = 16 * (k >> 1) + 4 * i + 2 * (k & 1);
+              pk[4 * k + i] = Elem<T>::pack2(v[x], v[x + 1]);
+              if (pl + 1 < PL) {
+                const float2 hi = Elem<T>::unpack2(pk[4 * k + i]);
+                v[x] -= hi.x;
+                v[x + 1] -= hi.y;
+              }
+            }
+          if (pl > 0) {  // the first plane's stores have finished reading the staging blocks
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            stsm_x4(sd_a + sw64(16 * (k >> 1) + 8 * (k & 1) + (lane & 7), 8 * (lane >> 3)), pk[4 * k], pk[4 * k + 1],
+                    pk[4 * k + 2], pk[4 * k + 3]);
+          if (diag || mirror) {
+            // the transposed block: matrix (h, s, i) lands at rows 8i.., columns 16h + 8s..
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              stsm_x4_trans(sm_a + sw64(lane, 16 * (k >> 1) + 8 * (k & 1)), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2],
+                            pk[4 * k + 3]);
+          }
+          if (diag) {
+            // symmetrise the diagonal block: above the diagonal (row < col)
+            // takes the value computed below it, from the transposed block
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j > lane)
+                *reinterpret_cast<uint16_t*>(sd + sw64(lane, j)) = *reinterpret_cast<const uint16_t*>(sm + sw64(lane, j));
+          }
+          fence_async_smem();  // generic-proxy writes become visible to the bulk copy
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&p.maps[g.mD], smem_u32(sd), c0, r0, t.b * PL + pl);
+            if (mirror) tma_store_3d(&p.maps[g.mD], smem_u32(sm), r0, c0, t.b * PL + pl);
+            bulk_commit();
+            ++groups;
+          }
         }
       }
       // this warp's TMEM reads are done: release the accumulator (to the
@@ -785,7 +841,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     // every producer has published its count and every early stop has
     // reached both abort flags; the follower stays resident (its shared
     // memory receives its own copies) until the leader's drain ends
-    if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<PAIR, BN>(full, issued_cnt, p.status);
+    if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<PAIR, BN, PL>(full, issued_cnt, p.status);
     __syncwarp();
     cluster_sync();
   }
@@ -923,11 +979,11 @@ EncodeTiledFn encode_fn() {
 }
 
 // 3-D map over [batch][outer][inner] with row stride ld and batch stride
-// (elements), box {box_inner, box_outer, 1}, zero fill out of range (loads)
+// (elements), box {box_inner, box_outer, box_batch}, zero fill out of range (loads)
 // and clipping (stores).
 bool make_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
               int64_t bstride, int box_outer, int box_inner = 64,
-              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, int box_batch = 1) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const CUtensorMapDataType dt = t == Op::BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -936,7 +992,7 @@ bool make_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t out
   const cuuint64_t es = op_size(t);
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)batch};
   cuuint64_t strides[2] = {(cuuint64_t)ld * es, (cuuint64_t)(batch > 1 ? bstride : ld * outer) * es};
-  cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer, (cuuint32_t)box_batch};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -957,16 +1013,16 @@ int current_device() {
 // Co-resident CTAs (PAIR = 1) or clusters (PAIR = 2) of the persistent
 // kernel on the current device; 0 if its attributes cannot be set. The
 // shared-memory attribute is set, and the count taken, once per device.
-template <typename T, int PAIR, int BN>
+template <typename T, int PAIR, int BN, int PL>
 int max_units() {
   static std::mutex mu;
   static int per_device[kMaxDevices];  // 0: not set up on that device yet
   const int dev = current_device();
   std::lock_guard<std::mutex> lock(mu);
   int& units = per_device[dev];
-  const void* fn = (const void*)tc::gemm_kernel<T, PAIR, BN>;
+  const void* fn = (const void*)tc::gemm_kernel<T, PAIR, BN, PL>;
   if (units == 0) {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, tc::Cfg<PAIR, BN>::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, tc::Cfg<PAIR, BN, PL>::SMEM) != cudaSuccess)
       return 0;
     int u = num_sms() / PAIR;
     if (PAIR == 2) {
@@ -975,7 +1031,7 @@ int max_units() {
       cudaLaunchConfig_t q = {};
       q.gridDim = dim3(2 * u);
       q.blockDim = dim3(tc::THREADS);
-      q.dynamicSmemBytes = tc::Cfg<PAIR, BN>::SMEM;
+      q.dynamicSmemBytes = tc::Cfg<PAIR, BN, PL>::SMEM;
       cudaLaunchAttribute a[1];
       a[0].id = cudaLaunchAttributeClusterDimension;
       a[0].val.clusterDim.x = 2;
@@ -993,13 +1049,13 @@ int max_units() {
   return units;
 }
 
-template <typename T, int PAIR, int BN>
+template <typename T, int PAIR, int BN, int PL>
 muon_status launch(const tc::Params& p, int total_tiles, int max_units, cudaStream_t s) {
   const int units = total_tiles < max_units ? total_tiles : max_units;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * PAIR);
   cfg.blockDim = dim3(tc::THREADS);
-  cfg.dynamicSmemBytes = tc::Cfg<PAIR, BN>::SMEM;
+  cfg.dynamicSmemBytes = tc::Cfg<PAIR, BN, PL>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1010,7 +1066,7 @@ muon_status launch(const tc::Params& p, int total_tiles, int max_units, cudaStre
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, tc::gemm_kernel<T, PAIR, BN>, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, tc::gemm_kernel<T, PAIR, BN, PL>, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 template <typename T>
@@ -1109,16 +1165,20 @@ size_t tc_split_scratch(int64_t n, int64_t K, int count) {
 }
 
 template <int BN>
-int units_for(Op t, int pair) {
-  if (pair == 2) return t == Op::BF16 ? max_units<__nv_bfloat16, 2, BN>() : max_units<__half, 2, BN>();
-  return t == Op::BF16 ? max_units<__nv_bfloat16, 1, BN>() : max_units<__half, 1, BN>();
+int units_for(Op t, int pair, int planes = 1) {
+  if (planes == 2) return pair == 2 ? max_units<__half, 2, BN, 2>() : max_units<__half, 1, BN, 2>();
+  if (pair == 2) return t == Op::BF16 ? max_units<__nv_bfloat16, 2, BN, 1>() : max_units<__half, 2, BN, 1>();
+  return t == Op::BF16 ? max_units<__nv_bfloat16, 1, BN, 1>() : max_units<__half, 1, BN, 1>();
 }
 
 template <int BN>
-muon_status launch_for(Op t, int pair, const tc::Params& p, int total, int units, cudaStream_t s) {
+muon_status launch_for(Op t, int pair, const tc::Params& p, int total, int units, cudaStream_t s, int planes = 1) {
+  if (planes == 2)
+    return pair == 2 ? launch<__half, 2, BN, 2>(p, total, units, s) : launch<__half, 1, BN, 2>(p, total, units, s);
   if (pair == 2)
-    return t == Op::BF16 ? launch<__nv_bfloat16, 2, BN>(p, total, units, s) : launch<__half, 2, BN>(p, total, units, s);
-  return t == Op::BF16 ? launch<__nv_bfloat16, 1, BN>(p, total, units, s) : launch<__half, 1, BN>(p, total, units, s);
+    return t == Op::BF16 ? launch<__nv_bfloat16, 2, BN, 1>(p, total, units, s)
+                         : launch<__half, 2, BN, 1>(p, total, units, s);
+  return t == Op::BF16 ? launch<__nv_bfloat16, 1, BN, 1>(p, total, units, s) : launch<__half, 1, BN, 1>(p, total, units, s);
 }
 
 namespace {
@@ -1129,11 +1189,11 @@ struct MapTable {
   struct Key {
     const void* base;
     int64_t inner, outer, batch, ld, bstride;
-    int box_outer, box_inner, swz, dt;
+    int box_outer, box_inner, swz, dt, box_batch;
     bool operator==(const Key& o) const {
       return base == o.base && inner == o.inner && outer == o.outer && batch == o.batch && ld == o.ld &&
              bstride == o.bstride && box_outer == o.box_outer && box_inner == o.box_inner && swz == o.swz &&
-             dt == o.dt;
+             dt == o.dt && box_batch == o.box_batch;
     }
   };
   tc::Params* p;
@@ -1141,12 +1201,13 @@ struct MapTable {
   // Index of the map (made on first use); -1 if it cannot be made or the
   // table is full.
   int get(Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld, int64_t bstride,
-          int box_outer, int box_inner = 64, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-    const Key k{base, inner, outer, batch, ld, bstride, box_outer, box_inner, (int)swz, (int)t};
+          int box_outer, int box_inner = 64, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, int box_batch = 1) {
+    const Key k{base, inner, outer, batch, ld, bstride, box_outer, box_inner, (int)swz, (int)t, box_batch};
     for (int i = 0; i < p->nmaps; ++i)
       if (keys[i] == k) return i;
     if (p->nmaps >= tc::kMaxMaps) return -1;
-    if (!make_map(&p->maps[p->nmaps], t, base, inner, outer, batch, ld, bstride, box_outer, box_inner, swz)) return -1;
+    if (!make_map(&p->maps[p->nmaps], t, base, inner, outer, batch, ld, bstride, box_outer, box_inner, swz, box_batch))
+      return -1;
     keys[p->nmaps] = k;
     return p->nmaps++;
   }
@@ -1158,11 +1219,15 @@ bool fill_job(tc::Job& g, const GemmDesc& d, Op t, int pair, int bn, int parts, 
   const int tile_m = tc::BM * pair;
   // A operand source: K-major [M][K], MN-major [K][M]; 128 rows per CTA.
   // B operand source: K-major [N][K], MN-major [K][N]; bn / pair rows per CTA.
-  g.mA = d.a_mn ? mt.get(t, d.A, d.M, d.K, d.batch, d.lda, d.strideA, 64)
-                : mt.get(t, d.A, d.K, d.M, d.batch, d.lda, d.strideA, tc::BM);
-  g.mB = d.b_mn ? mt.get(t, d.B, d.N, d.K, d.batch, d.ldb, d.strideB, 64)
-                : mt.get(t, d.B, d.K, d.N, d.batch, d.ldb, d.strideB, bn / pair);
-  g.mD = mt.get(t, d.D, d.N, d.M, d.batch, d.ldd, d.strideD, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  // Both planes of a matrix are neighbours along the batch dimension.
+  const int pl = d.planes == 2 ? 2 : 1;
+  const int64_t nb = (int64_t)d.batch * pl;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  g.mA = d.a_mn ? mt.get(t, d.A, d.M, d.K, nb, d.lda, d.strideA, 64, 64, sw, pl)
+                : mt.get(t, d.A, d.K, d.M, nb, d.lda, d.strideA, tc::BM, 64, sw, pl);
+  g.mB = d.b_mn ? mt.get(t, d.B, d.N, d.K, nb, d.ldb, d.strideB, 64, 64, sw, pl)
+                : mt.get(t, d.B, d.K, d.N, nb, d.ldb, d.strideB, bn / pair, 64, sw, pl);
+  g.mD = mt.get(t, d.D, d.N, d.M, nb, d.ldd, d.strideD, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   g.mP = -1;
   if (parts > 1) {
     const int64_t ldp = pad_ld(d.N);
@@ -1210,12 +1275,12 @@ muon_status check_desc(const GemmDesc& d) {
 bool has_work(const GemmDesc& d) { return d.batch > 0 && d.M > 0 && d.N > 0 && d.K > 0; }
 
 // Work accounting of one job (dense, symmetric-once and executed FLOPs).
-void count_job(const tc::Job& g, int tile_m, int bn) {
+void count_job(const tc::Job& g, int tile_m, int bn, int planes = 1) {
   Counters& cn = counters();
   const double mnk = (double)g.M * g.N * g.K * g.batch;
   cn.flops_dense += 2.0 * mnk;
   cn.flops_sym += g.sym ? mnk : 2.0 * mnk;
-  cn.flops_exec += 2.0 * tile_m * bn * (double)g.K * (g.tiles_per_batch / g.splits) * g.batch;
+  cn.flops_exec += 2.0 * tile_m * bn * (double)g.K * (g.tiles_per_batch / g.splits) * g.batch * (planes == 2 ? 3 : 1);
 }
 
 }  // namespace
@@ -1224,7 +1289,9 @@ muon_status tc_gemm(Op t, const GemmDesc* gd, int ngroups, int* status, uint64_t
   if (ngroups < 1 || ngroups > kMaxGemmGroups || (t != Op::BF16 && t != Op::F16)) return MUON_ERR_INVALID_ARG;
   const int pair = g_pair_mode;
   const int tile_m = tc::BM * pair;
-  int units = units_for<tc::BN_WIDE>(t, pair);
+  const int planes = gd[0].planes == 2 ? 2 : 1;  // the same for every group of a launch
+  if (planes == 2 && t != Op::F16) return MUON_ERR_INVALID_ARG;
+  int units = units_for<tc::BN_WIDE>(t, pair, planes);
   if (units <= 0) return MUON_ERR_CUDA;
 
   // the groups that have work, their tile counts at the wide tile width,
@@ -1247,7 +1314,7 @@ muon_status tc_gemm(Op t, const GemmDesc* gd, int ngroups, int* status, uint64_t
     const int nkb = (d.K + tc::BK - 1) / tc::BK;
     parts[i] = 1;
     kbps[i] = nkb;
-    if (!d.sym || !d.part) continue;
+    if (!d.sym || !d.part || planes == 2) continue;  // partial sums are reduced into one plane only
     int per = 0;
     const int n = split_parts(total_wide, units, nkb, &per);
     if (n < 2 || (size_t)n * d.batch * d.N * pad_ld(d.N) * sizeof(float) > d.part_bytes) continue;
@@ -1262,7 +1329,7 @@ muon_status tc_gemm(Op t, const GemmDesc* gd, int ngroups, int* status, uint64_t
   if (!any_split && total_wide < units) {
     int total_narrow = 0;
     for (int i = 0; i < ng; ++i) total_narrow += desc_tiles(*src[i], tile_m, tc::BN_NARROW) * src[i]->batch;
-    const int units_narrow = units_for<tc::BN_NARROW>(t, pair);
+    const int units_narrow = units_for<tc::BN_NARROW>(t, pair, planes);
     if (units_narrow <= 0) return MUON_ERR_CUDA;
     if (total_narrow > total_wide && total_narrow <= units_narrow) {
       bn = tc::BN_NARROW;
@@ -1325,9 +1392,9 @@ muon_status tc_gemm(Op t, const GemmDesc* gd, int ngroups, int* status, uint64_t
   Counters& cn = counters();
   cn.launches += sp.ngroups ? 2 : 1;
   cn.gemm_launches += 1;
-  for (int i = 0; i < ng; ++i) count_job(p.g[i], tile_m, bn);
-  const muon_status r = bn == tc::BN_WIDE ? launch_for<tc::BN_WIDE>(t, pair, p, total, units, s)
-                                          : launch_for<tc::BN_NARROW>(t, pair, p, total, units, s);
+  for (int i = 0; i < ng; ++i) count_job(p.g[i], tile_m, bn, planes);
+  const muon_status r = bn == tc::BN_WIDE ? launch_for<tc::BN_WIDE>(t, pair, p, total, units, s, planes)
+                                          : launch_for<tc::BN_NARROW>(t, pair, p, total, units, s, planes);
   if (r != MUON_OK || sp.ngroups == 0) return r;
   return t == Op::BF16 ? launch_reduce<__nv_bfloat16>(sp, red_blocks, s) : launch_reduce<__half>(sp, red_blocks, s);
 }

@@ -46,6 +46,10 @@ struct GemmDesc {
   int alpha_pow, beta_pow;
   float* part;
   size_t part_bytes;
+  // 2: every operand and the result are the sum of two fp16 planes, matrices
+  // 2b and 2b + 1 of their buffers (the strides are from plane to plane);
+  // K is not split then. 0 or 1: one plane.
+  int planes;
 };
 
 // Tensor-core GEMM (tcgen05 + TMEM + TMA), all groups in one persistent launch.
@@ -137,6 +141,11 @@ struct NsGroup {
   float rho;
   float* part;
   size_t part_bytes;
+  // planes = 2 (F16 operands, standard chain): every buffer holds two planes
+  // of each matrix, X[cur] holds kappa * X_0 on entry and kappa * O on return,
+  // and the n x n work matrices are stored times rho (xscale is not read).
+  int planes;
+  float kappa;
 };
 
 inline int ns_work_buffers(const muon_ns_params* p) { return p->gram ? 4 : 2; }

@@ -28,6 +28,11 @@ struct Shape {
   bool tall;
 };
 
+// Two planes (NsGroup::planes = 2): X is kept as kappa X and A, B as rho A,
+// rho B, so that both planes stay in fp16's normal range; the constants enter
+// the epilogues:  A <- (rho / kappa^2) X X^T,  B <- (c / rho) A A + b A,
+// X <- (1 / rho) B X + a X.
+
 Shape shape_of(const NsGroup& g) {
   Shape s;
   s.tall = g.rows > g.cols;
@@ -42,6 +47,7 @@ GemmDesc base(const NsGroup& g) {
   GemmDesc d{};
   d.batch = g.count;
   d.alpha = 1.f;
+  d.planes = g.planes;
   return d;
 }
 
@@ -143,14 +149,20 @@ muon_status run_standard(const Launcher& L, NsGroup* gs, int ng, const muon_ns_p
   for (int t = 0; t < p->T; ++t) {
     const float a = p->coeffs[t][0], b = p->coeffs[t][1], c = p->coeffs[t][2];
     const bool first = t == 0;
-    for (int i = 0; i < ng; ++i)
-      d[i] = gram_of(gs[i], gs[i].X[gs[i].cur], gs[i].nb[0], 1.f, first ? gs[i].xscale : nullptr, 2);
+    for (int i = 0; i < ng; ++i) {
+      const NsGroup& g = gs[i];
+      d[i] = g.planes == 2 ? gram_of(g, g.X[g.cur], g.nb[0], g.rho / (g.kappa * g.kappa), nullptr, 0)
+                           : gram_of(g, g.X[g.cur], g.nb[0], 1.f, first ? g.xscale : nullptr, 2);
+    }
     TRY(L(d, ng));
-    for (int i = 0; i < ng; ++i) d[i] = sym_of(gs[i], gs[i].nb[0], gs[i].nb[0], gs[i].nb[1], gs[i].nb[0], c, b, 0.f);
+    for (int i = 0; i < ng; ++i)
+      d[i] = sym_of(gs[i], gs[i].nb[0], gs[i].nb[0], gs[i].nb[1], gs[i].nb[0], gs[i].planes == 2 ? c / gs[i].rho : c, b,
+                    0.f);
     TRY(L(d, ng));
     for (int i = 0; i < ng; ++i) {
       NsGroup& g = gs[i];
-      d[i] = apply_of(g, g.nb[1], g.X[g.cur], g.X[g.cur ^ 1], 1.f, a, first ? g.xscale : nullptr, 1, 1);
+      d[i] = g.planes == 2 ? apply_of(g, g.nb[1], g.X[g.cur], g.X[g.cur ^ 1], 1.f / g.rho, a, nullptr, 0, 0)
+                           : apply_of(g, g.nb[1], g.X[g.cur], g.X[g.cur ^ 1], 1.f, a, first ? g.xscale : nullptr, 1, 1);
     }
     TRY(L(d, ng));
     for (int i = 0; i < ng; ++i) gs[i].cur ^= 1;
@@ -233,7 +245,8 @@ int ns_max_phases(const muon_ns_params* p) { return p->gram ? 4 * p->T + 4 : 3 *
 muon_status ns_run(Op t, NsGroup* gs, int ng, const muon_ns_params* p, int* status, uint64_t timeout_ns,
                    cudaStream_t s, unsigned* counters) {
   if (ng < 1 || ng > kMaxGemmGroups) return MUON_ERR_INVALID_ARG;
-  if (t == Op::F32 || !counters || !gemm_chain()) {
+  // two planes: one launch per product (the fused chain carries one plane)
+  if (t == Op::F32 || !counters || !gemm_chain() || gs[0].planes == 2) {
     const Launcher L{t, status, timeout_ns, s, nullptr};
     return p->gram ? run_gram(L, gs, ng, p) : run_standard(L, gs, ng, p);
   }

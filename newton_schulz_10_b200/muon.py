@@ -24,6 +24,7 @@ OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_DTYPE, ERR_ALIGN, ERR_WORKSPACE, ERR_CUDA, E
     ERR_TIMEOUT, ERR_UNSUPPORTED = range(10)
 # muon_dtype
 F32, BF16, F16 = 0, 1, 2
+F16X2 = 3  # compute type of the stack update: two fp16 planes per operand
 # muon_norm
 NORM_L1, NORM_L2 = 0, 1
 
@@ -32,7 +33,7 @@ EXPORTS = ("muon_set_wait_timeout_ns", "muon_set_gemm_cta_pair", "muon_status_st
            "select_rows", "muon_workspace_size", "muon_step", "muon_step_profiled", "muon_kernel_launch_count",
            "select_rows_noalloc", "muon_step_events", "muon_set_gemm_chain", "muon_momentum",
            "muon_orthogonalize", "muon_apply_update", "grouped_matmul", "grouped_matmul_dx", "grouped_matmul_dw",
-           "grouped_workspace_size")
+           "grouped_workspace_size", "muon_stack_params_default", "muon_stack_workspace_size", "muon_stack_step")
 
 
 class NsParams(C.Structure):
@@ -66,6 +67,19 @@ class Grouped(C.Structure):
     _fields_ = [("dtype", C.c_int32), ("experts", C.c_int32), ("tokens", C.c_int64), ("n", C.c_int64), ("k", C.c_int64),
                 ("ldx", C.c_int64), ("ldy", C.c_int64), ("ldw", C.c_int64), ("w_stride", C.c_int64),
                 ("offsets", C.c_void_p), ("dev_status", C.c_void_p)]
+
+
+class StackArray(C.Structure):
+    _fields_ = [("W", C.c_void_p), ("M", C.c_void_p), ("G", C.c_void_p), ("copy", C.c_void_p),
+                ("w_dtype", C.c_int32), ("g_dtype", C.c_int32), ("copy_dtype", C.c_int32),
+                ("count", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("w_stride", C.c_int64), ("w_ld", C.c_int64), ("m_stride", C.c_int64), ("m_ld", C.c_int64),
+                ("g_stride", C.c_int64), ("g_ld", C.c_int64), ("copy_stride", C.c_int64), ("copy_ld", C.c_int64)]
+
+
+class StackParams(C.Structure):
+    _fields_ = [("mu", C.c_float), ("lr", C.c_float), ("weight_decay", C.c_float), ("scale", C.c_float),
+                ("nesterov", C.c_int32), ("ns", NsParams), ("dev_status", C.c_void_p)]
 
 
 class MuonError(RuntimeError):
@@ -136,6 +150,12 @@ def lib() -> C.CDLL:
         L.grouped_matmul_dw.restype = i32
         L.grouped_workspace_size.argtypes = [i32]
         L.grouped_workspace_size.restype = sz
+        L.muon_stack_params_default.argtypes = [C.POINTER(StackParams)]
+        L.muon_stack_params_default.restype = None
+        L.muon_stack_workspace_size.argtypes = [C.POINTER(StackArray), i32, C.POINTER(StackParams)]
+        L.muon_stack_workspace_size.restype = sz
+        L.muon_stack_step.argtypes = [C.POINTER(StackArray), i32, C.POINTER(StackParams), vp, sz, vp]
+        L.muon_stack_step.restype = i32
         L.muon_kernel_launch_count.argtypes = []
         L.muon_kernel_launch_count.restype = i64
         _lib = L
@@ -528,3 +548,121 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
         _check(lib().grouped_matmul_dw(C.byref(g), _ptr(dy), _ptr(x), _ptr(out), _code_of(out, where), alpha, beta, _ptr(ws),
                                        ws.numel(), s), where)
     return out
+
+
+# ---------------------------------------------------------------------------
+# the update of stacks of matrices
+# ---------------------------------------------------------------------------
+
+
+def stack_params(mu: float = 0.95, lr: float = 0.02, weight_decay: float = 0.0, scale: float = 1.0, nesterov: bool = False,
+                 ns: NsParams | None = None, dev_status=None) -> StackParams:
+    """Parameters of a stack update; ns.compute may be F16X2 (two fp16 planes
+    per operand: about fp32 accuracy on the tensor cores)."""
+    p = StackParams()
+    lib().muon_stack_params_default(C.byref(p))
+    p.mu, p.lr, p.weight_decay, p.scale, p.nesterov = mu, lr, weight_decay, scale, int(nesterov)
+    if ns is not None:
+        p.ns = ns
+    p.dev_status = None if dev_status is None else _ptr(dev_status)
+    return p
+
+
+@dataclass
+class Stack:
+    """count x rows x cols tensors (views with any strides and adjacent
+    columns): weights W (fp32, bf16 or fp16), fp32 momentum M, gradient G
+    (fp32, bf16, fp16; None when the momentum already holds it) and an
+    optional 16-bit copy of the new weights."""
+    W: object
+    M: object
+    G: object = None
+    copy: object = None
+
+
+def _stacks(stacks, where: str):
+    import torch
+    arr = (StackArray * max(len(stacks), 1))()
+    for i, k in enumerate(stacks):
+        shape = k.W.shape
+        _need(len(shape) == 3, ERR_SHAPE, where)
+        given = [t for t in (k.W, k.M, k.G, k.copy) if t is not None]
+        _need(k.M is not None and all(t.shape == shape for t in given), ERR_SHAPE, where)
+        _need(shape[2] <= 1 or all(t.stride(2) == 1 for t in given), ERR_SHAPE, where)
+        _need(k.M.dtype == torch.float32, ERR_DTYPE, where)
+        _need(all(t.is_cuda and t.device == stacks[0].W.device for t in given), ERR_INVALID_ARG, where)
+        a = arr[i]
+        a.W, a.M, a.G, a.copy = _ptr(k.W), _ptr(k.M), _ptr(k.G), _ptr(k.copy)
+        a.count, a.rows, a.cols = shape
+        a.w_dtype, a.w_stride, a.w_ld = _code_of(k.W, where), k.W.stride(0), k.W.stride(1)
+        a.m_stride, a.m_ld = k.M.stride(0), k.M.stride(1)
+        if k.G is not None:
+            a.g_dtype, a.g_stride, a.g_ld = _code_of(k.G, where), k.G.stride(0), k.G.stride(1)
+        if k.copy is not None:
+            a.copy_dtype, a.copy_stride, a.copy_ld = _code_of(k.copy, where), k.copy.stride(0), k.copy.stride(1)
+    return arr
+
+
+@dataclass
+class StackStep:
+    """A prepared update of stacks: the table and a workspace, reused by every
+    call. The tensors are updated in place:
+
+        step = StackStep([Stack(W, M, G)], stack_params(...))
+        step()                                # M, W from this step's G
+        step = StackStep([Stack(W, M)], ...)  # no gradient tensor:
+        step.accumulate(0, dy, x, offsets)    # M <- mu M + dy_e^T x_e
+        step()                                # W from M
+    """
+    stacks: list
+    params: StackParams
+    ws: object = None
+    _table: object = field(default=None, repr=False)
+    _grouped_ws: list = field(default=None, repr=False)
+
+    def __post_init__(self):
+        where = "muon_stack_step"
+        self._table = _stacks(self.stacks, where)
+        self._grouped_ws = [None] * len(self.stacks)
+        if self.ws is None:
+            import torch
+            device = self.stacks[0].W.device if self.stacks else "cuda"
+            if self.stacks:
+                with torch.cuda.device(device):
+                    n = lib().muon_stack_workspace_size(self._table, len(self.stacks), C.byref(self.params))
+                _need(n > 0, ERR_INVALID_ARG, "muon_stack_workspace_size")
+            else:
+                n = 0
+            self.ws = workspace(n, device)
+
+    def __call__(self, stream=None) -> None:
+        if not self.stacks:
+            return
+        dev, s = _call_stream(self.stacks[0].W, stream)
+        with dev:
+            _check(lib().muon_stack_step(self._table, len(self.stacks), C.byref(self.params), _ptr(self.ws), self.ws.numel(),
+                                         s), "muon_stack_step")
+
+    def accumulate(self, i: int, dy, x, offsets, stream=None) -> None:
+        """M <- mu M + dy_e^T x_e for the experts of stack i, whose G is None:
+        the momentum step straight from an expert layer's rows."""
+        k = self.stacks[i]
+        _need(k.G is None, ERR_INVALID_ARG, "StackStep.accumulate")
+        if self._grouped_ws[i] is None:
+            self._grouped_ws[i] = workspace(grouped_workspace_size(k.M.shape[0]), k.M.device)
+        grouped_matmul_dw(dy, x, offsets, out=k.M, beta=self.params.mu, ws=self._grouped_ws[i], stream=stream)
+
+    def device_status(self) -> int:
+        """Deferred device status of the last step (synchronises)."""
+        import torch
+        if self.params.dev_status:
+            raise RuntimeError("status goes to the caller's dev_status")
+        return int(self.ws[:4].view(torch.int32).item())
+
+
+def stack_step(stacks, p: StackParams | None = None, ws=None, stream=None) -> StackStep:
+    """One update of stacks = [Stack(W, M, G[, copy]), ...]. Returns the
+    StackStep (reusable)."""
+    s = StackStep(list(stacks), p or stack_params(), ws)
+    s(stream)
+    return s

@@ -1,0 +1,293 @@
+"""The update of stacks of matrices against its formulas in 64 bits.
+
+Tolerances of O are the framework's own, relative in the Frobenius norm:
+1e-4 for two fp16 planes (the bound of the fp32 paths: every rounding of that
+chain is 2^-11 of the fp16 chain's, which stays below 1e-2) and for fp32, 2e-2
+for bf16 and fp16. An element of O is then off by at most tol ||O||_F. The
+update adds one rounding to W's type (half a step) and two fp32 roundings of
+the sum's terms (2^-23 of each).
+"""
+
+import math
+
+import pytest
+import torch
+
+from newton_schulz_10_b200 import muon as mu
+
+pytestmark = pytest.mark.gpu
+
+ABC = (3.4445, -4.7750, 2.0315)
+TOL = {mu.F16X2: 1e-4, mu.F32: 1e-4, mu.BF16: 2e-2, mu.F16: 2e-2}
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def polar(X, eps=1e-7, T=5):
+    a, b, c = ABC
+    X = X.double()
+    tall = X.shape[-2] > X.shape[-1]
+    X = X.mT if tall else X
+    norm = X.square().sum((-2, -1), keepdim=True).sqrt()
+    X = torch.where(norm > 0, X / (norm + eps), torch.zeros_like(X))
+    for _ in range(T):
+        A = X @ X.mT
+        X = a * X + (b * A + c * A @ A) @ X
+    return X.mT if tall else X
+
+
+def gauss(shape, seed, std=1.0, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def spectrum(shape, seed, std=1.0):
+    """Strong directions over noise, 16 to 1."""
+    c, r, m = shape
+    k = max(1, min(r, m) // 16)
+    low = gauss((c, r, k), seed) @ gauss((c, k, m), seed + 1)
+    return (low * (4.0 / math.sqrt(k)) + 0.25 * gauss(shape, seed + 2)) * std
+
+
+LAYOUTS = ("dense", "padded", "beside", "gap")
+
+
+def laid_out(t, layout):
+    """The same values as a view of a wider tensor of NaN, and that tensor."""
+    c, r, m = t.shape
+    if layout == "dense":
+        return t.clone(), None
+    if layout == "padded":  # rows 5 elements wider, 3 rows between matrices
+        wide = torch.full((c, r + 3, m + 5), float("nan"), dtype=t.dtype, device=t.device)
+        view = wide[:, :r, :m]
+    elif layout == "beside":  # column blocks of one matrix
+        wide = torch.full((r, c * m + 7), float("nan"), dtype=t.dtype, device=t.device)
+        view = wide[:, :c * m].view(r, c, m).permute(1, 0, 2)
+    else:  # rows 8 elements wider: aligned vectors with a gap
+        wide = torch.full((c, r, (m + 15) // 8 * 8), float("nan"), dtype=t.dtype, device=t.device)
+        view = wide[:, :, :m]
+    view.copy_(t)
+    return view, wide
+
+
+def rel(a, b):
+    return ((a.double() - b).norm() / b.norm().clamp_min(1e-300)).item()
+
+
+SHAPES = [(1, 1, 1), (3, 1, 40), (2, 40, 1), (3, 64, 64), (5, 33, 200), (4, 200, 33), (2, 130, 257), (12, 64, 768), (2, 520, 264)]
+
+
+@pytest.mark.parametrize("compute", [mu.F16X2, mu.BF16, mu.F16, mu.F32])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_orthogonalised_update(cuda, shape, compute):
+    """W = 0, lr scale = -1: the new W is O itself."""
+    M = spectrum(shape, 11, 1e-3) if compute in (mu.F16X2, mu.F32) else gauss(shape, 11, 1e-3)
+    W = torch.zeros(shape, device="cuda")
+    step = mu.stack_step([mu.Stack(W, M.clone())], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(compute=compute)))
+    want = polar(M)
+    assert step.device_status() == mu.OK
+    for i in range(shape[0]):
+        assert rel(W[i], want[i]) <= TOL[compute], i
+
+
+@pytest.mark.parametrize("gram,compute", [(True, mu.F16), (True, mu.BF16), (True, mu.F32)])
+def test_gram_chain(cuda, gram, compute):
+    M = gauss((3, 96, 300), 12, 1e-3)
+    W = torch.zeros_like(M)
+    mu.stack_step([mu.Stack(W, M.clone())], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(gram=True, compute=compute)))
+    assert rel(W, polar(M)) <= TOL[compute]
+
+
+def check_update(W0, M0, G, W, M, copy, p, tol):
+    lr, wd, sc = p.lr, p.weight_decay, p.scale
+    m = M0.double() if G is None else p.mu * M0.double() + G.double()
+    assert bool(((M.double() - m).abs() <= 2.0 ** -23 * m.abs() + 2.0 ** -149).all())
+    X = G.double() + p.mu * M.double() if p.nesterov else M.double()
+    O = polar(X)
+    want = (1 - lr * wd) * W0.double() - lr * sc * O
+    norm = O.square().sum((-2, -1), keepdim=True).sqrt()
+    base = 2.0 ** -22 * (W0.double().abs() + abs(lr * sc) * O.abs()) + abs(lr * sc) * tol * norm
+    for got in (W, copy):
+        if got is None:
+            continue
+        tiny = 2.0 ** -25 if got.dtype == torch.float16 else 0.0
+        assert bool(((got.double() - want).abs() <= 1.01 * (torch.finfo(got.dtype).eps / 2 * want.abs() + base) + tiny).all())
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("w,g,copy,nesterov,decay", [("f32", "f32", None, False, 0.0), ("f32", "bf16", "bf16", True, 0.1),
+                                                     ("bf16", "bf16", None, True, 0.1), ("f16", "f16", "bf16", False, 0.3),
+                                                     ("f32", None, "f16", False, 0.1), ("bf16", "f32", None, True, 0.0)])
+@pytest.mark.parametrize("shape", [(3, 48, 80), (4, 37, 21), (2, 24, 4100)], ids=str)
+@pytest.mark.parametrize("compute", [mu.F16X2, mu.BF16])
+def test_whole_update(cuda, shape, w, g, copy, nesterov, decay, layout, compute):
+    W0, M0 = gauss(shape, 21, 0.02, DT[w]), gauss(shape, 22, 1e-2)
+    G = gauss(shape, 23, 1e-2, DT[g]) if g else None
+    (W, Wb), (M, Mb) = laid_out(W0, layout), laid_out(M0, layout)
+    Gv, Gb = laid_out(G, layout) if g else (None, None)
+    C, Cb = laid_out(torch.zeros(shape, dtype=DT[copy], device="cuda"), layout) if copy else (None, None)
+    p = mu.stack_params(mu=0.9, lr=0.01, weight_decay=decay, scale=3.0, nesterov=nesterov, ns=mu.ns_params(compute=compute))
+    behind = [(b, b.isnan().sum()) for b in (Wb, Mb, Cb) if b is not None]
+    step = mu.stack_step([mu.Stack(W, M, Gv, C)], p)
+    assert step.device_status() == mu.OK
+    check_update(W0, M0, G, W, M, C, p, TOL[compute])
+    for b, n in behind:
+        assert torch.equal(b.isnan().sum(), n)  # nothing between the rows is written
+    if g:
+        assert torch.equal(Gv, G)
+
+
+def test_several_stacks_and_empty_ones(cuda):
+    """More stacks than one launch's shape groups, some empty, each as if alone."""
+    shapes = [(2, 40, 24), (0, 8, 8), (3, 24, 40), (1, 64, 200), (4, 0, 16), (1, 200, 64), (2, 96, 96), (1, 17, 5), (2, 3, 0)]
+    for compute in (mu.F16X2, mu.BF16):
+        p = mu.stack_params(nesterov=True, weight_decay=0.1, ns=mu.ns_params(compute=compute))
+        a = [mu.Stack(gauss(s, 31, 0.02), gauss(s, 32), gauss(s, 33)) for s in shapes]
+        b = [mu.Stack(k.W.clone(), k.M.clone(), k.G) for k in a]
+        step = mu.stack_step(a, p)
+        assert step.device_status() == mu.OK
+        for x, y in zip(a, b):
+            mu.stack_step([y], p)
+            assert torch.equal(x.M, y.M)
+            # a tile width or a split of K that goes by the launch's size may order the sums differently
+            if x.W.numel():
+                assert rel(x.W, y.W.double()) <= (1e-6 if compute == mu.F16X2 else 1e-4)
+
+
+@pytest.mark.parametrize("compute", [mu.F16X2, mu.BF16, mu.F16])
+def test_zero_small_and_large_matrices(cuda, compute):
+    """A matrix of zeros is left alone (with eps 0 too), a tiny or huge one is orthogonalised like any other."""
+    M = gauss((5, 48, 64), 41)
+    M[1] = 0
+    M[2] *= 1e-6
+    M[3] *= 1e15 if compute == mu.BF16 else 1e30
+    M[4] = 0
+    M[4, 3, 5] = 2.0
+    for eps in (1e-7, 0.0):
+        W = torch.ones_like(M)
+        step = mu.stack_step([mu.Stack(W, M.clone())], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(compute=compute, norm_eps=eps)))
+        assert step.device_status() == mu.OK
+        assert bool((W[1] == 1).all())
+        want = polar(M, eps)
+        for i in (0, 2, 3, 4):
+            # 1 + O in fp32: half a step of 1 an element beside O's own error
+            assert (W[i].double() - 1 - want[i]).norm() <= TOL[compute] * want[i].norm() + 2.0 ** -23 * math.sqrt(48 * 64)
+
+
+def test_nonfinite_matrix_is_reported_and_stays_alone(cuda):
+    M = gauss((3, 40, 56), 51)
+    W, ref = gauss(M.shape, 52), None
+    p = mu.stack_params(ns=mu.ns_params(compute=mu.F16X2))
+    good = W.clone()
+    mu.stack_step([mu.Stack(good, M.clone())], p)
+    M2 = M.clone()
+    M2[1, 3, 7] = float("nan")
+    W2 = W.clone()
+    step = mu.stack_step([mu.Stack(W2, M2)], p)
+    assert step.device_status() == mu.ERR_NONFINITE
+    assert torch.equal(W2[0], good[0]) and torch.equal(W2[2], good[2])
+
+
+def test_overflowing_polynomial_is_reported(cuda):
+    W, M = torch.zeros((2, 64, 64), device="cuda"), gauss((2, 64, 64), 53)
+    for compute in (mu.F16X2, mu.F16):
+        step = mu.stack_step([mu.Stack(W.clone(), M.clone())],
+                             mu.stack_params(ns=mu.ns_params(compute=compute, coeffs=(3000.0, 0.0, 0.0))))
+        assert step.device_status() == mu.ERR_NONFINITE
+
+
+def test_repeated_gradient_and_single_matrix(cuda):
+    """G may be one matrix for the whole stack (stride 0); a padded single matrix is a stack of one."""
+    g = gauss((1, 32, 48), 61)
+    W0, M0 = gauss((4, 32, 48), 62, 0.02), gauss((4, 32, 48), 63)
+    W, M = W0.clone(), M0.clone()
+    p = mu.stack_params(nesterov=True, ns=mu.ns_params(compute=mu.F16X2))
+    mu.stack_step([mu.Stack(W, M, g.expand(4, 32, 48))], p)
+    check_update(W0, M0, g.expand(4, 32, 48), W, M, None, p, TOL[mu.F16X2])
+
+
+def test_graph_replay_and_two_steps(cuda):
+    shapes = [(3, 64, 96), (2, 100, 40)]
+    p = mu.stack_params(nesterov=True, weight_decay=0.1, ns=mu.ns_params(compute=mu.F16X2))
+
+    def make():
+        return [mu.Stack(gauss(s, 71, 0.02), gauss(s, 72), gauss(s, 73, dtype=torch.bfloat16), gauss(s, 74, dtype=torch.bfloat16)) for s in shapes]
+
+    a, b = make(), make()
+    eager, captured = mu.StackStep(a, p), mu.StackStep(b, p)
+    warm = mu.StackStep(make(), p)
+    warm()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured()
+    for _ in range(2):
+        eager()
+        graph.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(a, b):
+        assert torch.equal(x.W, y.W) and torch.equal(x.M, y.M) and torch.equal(x.copy, y.copy)
+
+
+def test_agrees_with_the_matrix_step(cuda):
+    """Plain fp32 tensors: the same update as muon_step, matrix by matrix."""
+    for compute in (mu.BF16, mu.F16):
+        W, M, G = gauss((3, 96, 160), 81, 0.02), gauss((3, 96, 160), 82), gauss((3, 96, 160), 83)
+        a = [(W[i].clone(), M[i].clone(), G[i].clone()) for i in range(3)]
+        ns = mu.ns_params(compute=compute)
+        mu.muon_step(a, mu.step_params(mu=0.95, lr=0.02, ns=ns))
+        W0 = W.clone()
+        mu.stack_step([mu.Stack(W, M, G)], mu.stack_params(mu=0.95, lr=0.02, ns=ns))
+        for i in range(3):
+            assert torch.equal(M[i], a[i][1])
+            # the row sums are added in another order: the scale may differ in its last bit
+            assert rel(W[i] - W0[i], (a[i][0] - W0[i]).double()) <= 1e-3
+
+
+@pytest.mark.parametrize("copy", [None, "bf16"])
+def test_expert_layer_step(cuda, copy):
+    """Together: forward, both gradients (the weights' into the momentum), update of the expert stack."""
+    d = torch.bfloat16
+    counts = [70, 0, 131, 7]
+    off = torch.tensor([0, 70, 70, 201, 208], dtype=torch.int32, device="cuda")
+    n, k = 96, 136
+    W0 = gauss((4, n, k), 91, 0.05)
+    W, M = W0.clone(), gauss((4, n, k), 92, 1e-2)
+    M[1] = 0  # the expert without rows never had any
+    M0 = M.clone()
+    w = W.to(d)
+    x, dy = gauss((208, k), 93, dtype=d), gauss((208, n), 94, 1e-2, dtype=d)
+    p = mu.stack_params(mu=0.9, lr=0.01, weight_decay=0.1, scale=2.0, ns=mu.ns_params(compute=mu.F16X2))
+    step = mu.StackStep([mu.Stack(W, M, None, w if copy else None)], p)
+    y, dx = mu.grouped_matmul(x, w, off), mu.grouped_matmul_dx(dy, w, off)
+    w_used = w.clone()
+    step.accumulate(0, dy, x, off)
+    step()
+    assert step.device_status() == mu.OK
+    m = 0.9 * M0.double()
+    for e in range(4):
+        r = slice(int(off[e]), int(off[e + 1]))
+        assert rel(y[r], x[r].double() @ w_used[e].double().T) <= 2.0 ** -8 if counts[e] else True
+        assert rel(dx[r], dy[r].double() @ w_used[e].double()) <= 2.0 ** -8 if counts[e] else True
+        m[e] += dy[r].double().T @ x[r].double()
+    # p.mu is 0.9 in fp32; sums of up to 131 products and two roundings
+    assert (M.double() - m).norm() <= 2.0 ** -21 * m.norm() + (131 / 16 + 8) * 2.0 ** -23 * (dy.double().abs().T @ x.double().abs()).norm()
+    assert bool((M[1] == 0).all())
+    check_update(W0, M.clone(), None, W, M, w if copy else None, p, TOL[mu.F16X2])
+    if copy:
+        assert not torch.equal(w, w_used)
+
+
+def test_on_another_stream(cuda):
+    p = mu.stack_params(nesterov=True, ns=mu.ns_params(compute=mu.F16X2))
+    W, M, G = gauss((3, 80, 120), 95, 0.02), gauss((3, 80, 120), 96), gauss((3, 80, 120), 97)
+    W1, M1 = W.clone(), M.clone()
+    mu.stack_step([mu.Stack(W1, M1, G)], p)
+    W2, M2, G2 = W.clone(), M.clone(), torch.zeros_like(G)
+    step = mu.StackStep([mu.Stack(W2, M2, G2)], p)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        G2.copy_(G)
+        step()
+    s.synchronize()
+    assert torch.equal(W1, W2) and torch.equal(M1, M2)
