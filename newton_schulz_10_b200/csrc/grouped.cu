@@ -53,6 +53,13 @@ constexpr int TMEM_COLS = 512;
 constexpr int ACC_COLS = 256;
 constexpr int kMaxExperts = 1024;
 constexpr uint64_t DRAIN_NS = 1000000000ull;
+// The tensor core truncates each addition to an fp32 accumulator, which
+// shrinks a long sum a little with every instruction (measured: an fp32 dW of
+// 1024 rows is 9.7e-7 off, in proportion to the rows). Sums into fp32 outputs
+// are therefore cut every 512 rows (8 k-blocks) and the parts added with
+// rounding to nearest, in order, by the same threads; a part's epilogue
+// overlaps the next part's products.
+constexpr int kPartBlocks = 8;
 
 enum : int { ROWS = 0, DW = 1 };
 
@@ -153,6 +160,13 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* tile_begin, i
     t.nkb = (s.end - s.begin + BK - 1) / BK;
   }
   return t;
+}
+
+// Parts that a tile's sum is cut into (kPartBlocks).
+template <int MODE, typename O>
+__device__ __forceinline__ int parts_of(int nkb) {
+  if (MODE == DW && std::is_same<O, float>::value && nkb > kPartBlocks) return (nkb + kPartBlocks - 1) / kPartBlocks;
+  return 1;
 }
 
 __device__ __forceinline__ uint32_t sw64(int r, int c) {
@@ -434,13 +448,17 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     for (int tile = unit; tile < total && ok; tile += units) {
       const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
       const uint32_t idesc = idesc_f16(fmt, a_mn, b_mn, TILE_M, t.n_mma);
+      const int parts = parts_of<MODE, O>(t.nkb);
+      for (int part = 0; part < parts && ok; ++part) {
       if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, budget, p.status)) {
         raise_peer();
+        ok = false;
         break;
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
-      for (int kb = 0; kb < t.nkb; ++kb) {
+      const int kb0 = part * kPartBlocks, kb1 = part + 1 < parts ? kb0 + kPartBlocks : t.nkb;
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag, budget, p.status)) {
           raise_peer();
           ok = false;
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < BK / UMMA_K; ++k)
           umma_f16_pair(d_tmem, a_hi | (uint64_t)(a_lo + k * (a_kstep >> 4)), b_hi | (uint64_t)(b_lo + k * (b_kstep >> 4)),
-                        idesc, kb != 0 || k != 0);
+                        idesc, kb != kb0 || k != 0);
         umma_commit_pair(&empty[stage], 0x3);
         if (++stage == STAGES) {
           stage = 0;
@@ -462,6 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
+      }
       }
     }
     umma_commit_pair(drain, 0x3);
@@ -476,10 +495,15 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     const uint32_t sd_a = smem_u32(sd);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int tile = unit; tile < total; tile += units) {
+    bool go = true;
+    for (int tile = unit; tile < total && go; tile += units) {
       const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
+      const int parts = parts_of<MODE, O>(t.nkb);
+      for (int part = 0; part < parts; ++part) {
+      const float beta = part == 0 ? p.beta : 1.f;
       const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, budget, p.status);
-      if (!__all_sync(0xffffffffu, ok)) {
+      go = __all_sync(0xffffffffu, ok);
+      if (!go) {
         if (lane == 0) raise_peer();
         break;
       }
@@ -537,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
           if (r0 >= p.M || c0 >= p.N) break;  // warp-uniform
           const int cc = c0 + (lane & 7) * 4;
           float4 old[8];
-          if (p.beta != 0.f) {
+          if (beta != 0.f) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int r = r0 + 4 * j + (lane >> 3);
@@ -575,9 +599,9 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
             if (r >= p.M || cc >= p.N) continue;
             float4 v = *reinterpret_cast<const float4*>(sd + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
             v.x *= p.alpha; v.y *= p.alpha; v.z *= p.alpha; v.w *= p.alpha;
-            if (p.beta != 0.f) {
-              v.x = fmaf(p.beta, old[j].x, v.x); v.y = fmaf(p.beta, old[j].y, v.y);
-              v.z = fmaf(p.beta, old[j].z, v.z); v.w = fmaf(p.beta, old[j].w, v.w);
+            if (beta != 0.f) {
+              v.x = fmaf(beta, old[j].x, v.x); v.y = fmaf(beta, old[j].y, v.y);
+              v.z = fmaf(beta, old[j].z, v.z); v.w = fmaf(beta, old[j].w, v.w);
             }
             O* d = out + (long long)r * p.ldo + cc;
             if (p.vec && cc + 4 <= p.N) {
@@ -600,6 +624,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
+      }
       }
     }
   }

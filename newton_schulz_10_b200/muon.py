@@ -453,43 +453,52 @@ def _code_of(t, where: str) -> int:
     return code
 
 
-def _call_stream(t, stream):
-    """The CUDA device of t and the stream of the call: the given one, else
-    the current stream of that device (whatever device is current)."""
+def _call_on(device: int, stream, fn, args, where: str) -> None:
+    """fn(*args, stream) with the CUDA device of the tensors current, on the
+    given stream or that device's current one. The raw stream handle and the
+    comparison with the current device keep this at about a microsecond,
+    which a call of a few tokens would notice."""
     import torch
-    return torch.cuda.device(t.device), _stream(torch.cuda.current_stream(t.device) if stream is None else stream)
-
-
-def _row_stride(t, where: str) -> int:
-    """Row stride of a matrix (or of each matrix of a stack) with unit column stride."""
-    _need(t.shape[-1] == 1 or t.stride(-1) == 1, ERR_SHAPE, where)
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if torch.cuda.current_device() == device:
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, raw)
+    if code != OK:
+        raise MuonError(code, where)
 
 
 def _grouped(where, x, y, w, offsets, dev_status):
-    """The descriptor of a call: x (tokens, k), y (tokens, n), w (experts, n, k)."""
+    """The descriptor and device of a call: x (tokens, k), y (tokens, n), w (experts, n, k)."""
     import torch
-    _need(x.dim() == 2 and y.dim() == 2 and w.dim() == 3 and offsets.dim() == 1, ERR_SHAPE, where)
-    experts, n, k = w.shape
-    _need(x.shape[1] == k and y.shape == (x.shape[0], n) and offsets.shape[0] == experts + 1, ERR_SHAPE, where)
-    _need(x.dtype == y.dtype and x.dtype in (torch.bfloat16, torch.float16) and offsets.dtype == torch.int32, ERR_DTYPE, where)
-    _need(all(t.is_cuda and t.device == x.device for t in (x, y, w, offsets)) and offsets.is_contiguous(), ERR_INVALID_ARG, where)
-    if dev_status is not None:
-        _need(dev_status.dtype == torch.int32 and dev_status.device == x.device, ERR_INVALID_ARG, where)
-
-    def ld(t):
-        # the stride of a single row is never used: any aligned value will do
-        return _row_stride(t, where) if t.shape[-2] > 1 else -(-t.shape[-1] // 8) * 8
-
-    return Grouped(_code_of(x, where), experts, x.shape[0], n, k, ld(x), ld(y), ld(w), w.stride(0) if experts > 1 else 0,
-                   _ptr(offsets), _ptr(dev_status))
-
-
-def _grouped_out(out, shape, like):
-    import torch
-    if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    return out
+    xs, ys, ws, os_ = x.shape, y.shape, w.shape, offsets.shape
+    if len(xs) != 2 or len(ys) != 2 or len(ws) != 3 or len(os_) != 1:
+        raise MuonError(ERR_SHAPE, where)
+    tokens, k = xs
+    experts, n, wk = ws
+    if wk != k or ys[0] != tokens or ys[1] != n or os_[0] != experts + 1:
+        raise MuonError(ERR_SHAPE, where)
+    dtype = x.dtype
+    if y.dtype != dtype or (dtype != torch.bfloat16 and dtype != torch.float16) or offsets.dtype != torch.int32:
+        raise MuonError(ERR_DTYPE, where)
+    device = x.get_device()
+    if device < 0 or y.get_device() != device or w.get_device() != device or offsets.get_device() != device:
+        raise MuonError(ERR_INVALID_ARG, where)
+    xt, yt, wt = x.stride(), y.stride(), w.stride()
+    if (k > 1 and (xt[1] != 1 or wt[2] != 1)) or (n > 1 and yt[1] != 1) or (experts > 0 and offsets.stride(0) != 1):
+        raise MuonError(ERR_SHAPE, where)
+    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.get_device() != device):
+        raise MuonError(ERR_INVALID_ARG, where)
+    # the stride of a single row is never used: any aligned value will do
+    kp, np_ = (k + 7) & ~7, (n + 7) & ~7
+    g = Grouped(BF16 if dtype == torch.bfloat16 else F16, experts, tokens, n, k, xt[0] if tokens > 1 else kp,
+                yt[0] if tokens > 1 else np_, wt[1] if n > 1 else kp, wt[0] if experts > 1 else 0, offsets.data_ptr(),
+                None if dev_status is None else dev_status.data_ptr())
+    return g, device
 
 
 def grouped_matmul(x, w, offsets, out=None, dev_status=None, stream=None):
@@ -500,26 +509,26 @@ def grouped_matmul(x, w, offsets, out=None, dev_status=None, stream=None):
     (experts + 1, int32, on the device) each expert's first row. Rows of `out`
     (tokens, n) that belong to no expert keep their values."""
     where = "grouped_matmul"
-    _need(x.dim() == 2 and w.dim() == 3, ERR_SHAPE, where)
-    y = _grouped_out(out, (x.shape[0], w.shape[1]), x)
-    _need(w.dtype == x.dtype, ERR_DTYPE, where)
-    g = _grouped(where, x, y, w, offsets, dev_status)
-    dev, s = _call_stream(x, stream)
-    with dev:
-        _check(lib().grouped_matmul(C.byref(g), _ptr(x), _ptr(w), _ptr(y), s), where)
+    if x.dim() != 2 or w.dim() != 3:
+        raise MuonError(ERR_SHAPE, where)
+    if w.dtype != x.dtype:
+        raise MuonError(ERR_DTYPE, where)
+    y = x.new_empty((x.shape[0], w.shape[1])) if out is None else out
+    g, device = _grouped(where, x, y, w, offsets, dev_status)
+    _call_on(device, stream, lib().grouped_matmul, (C.byref(g), x.data_ptr(), w.data_ptr(), y.data_ptr()), where)
     return y
 
 
 def grouped_matmul_dx(dy, w, offsets, out=None, dev_status=None, stream=None):
     """dx[r] = dy[r] @ w[e]: the gradient of grouped_matmul for its rows."""
     where = "grouped_matmul_dx"
-    _need(dy.dim() == 2 and w.dim() == 3, ERR_SHAPE, where)
-    dx = _grouped_out(out, (dy.shape[0], w.shape[2]), dy)
-    _need(w.dtype == dy.dtype, ERR_DTYPE, where)
-    g = _grouped(where, dx, dy, w, offsets, dev_status)
-    dev, s = _call_stream(dy, stream)
-    with dev:
-        _check(lib().grouped_matmul_dx(C.byref(g), _ptr(dy), _ptr(w), _ptr(dx), s), where)
+    if dy.dim() != 2 or w.dim() != 3:
+        raise MuonError(ERR_SHAPE, where)
+    if w.dtype != dy.dtype:
+        raise MuonError(ERR_DTYPE, where)
+    dx = dy.new_empty((dy.shape[0], w.shape[2])) if out is None else out
+    g, device = _grouped(where, dx, dy, w, offsets, dev_status)
+    _call_on(device, stream, lib().grouped_matmul_dx, (C.byref(g), dy.data_ptr(), w.data_ptr(), dx.data_ptr()), where)
     return dx
 
 
@@ -540,13 +549,11 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
     if out is None:
         _need(beta == 0.0, ERR_INVALID_ARG, where)
         out = torch.empty((experts, dy.shape[1], -(-x.shape[1] // 8) * 8), dtype=torch.float32, device=x.device)[:, :, :x.shape[1]]
-    g = _grouped(where, x, dy, out, offsets, dev_status)
+    g, device = _grouped(where, x, dy, out, offsets, dev_status)
     if ws is None:
         ws = workspace(grouped_workspace_size(experts), x.device)
-    dev, s = _call_stream(x, stream)
-    with dev:
-        _check(lib().grouped_matmul_dw(C.byref(g), _ptr(dy), _ptr(x), _ptr(out), _code_of(out, where), alpha, beta, _ptr(ws),
-                                       ws.numel(), s), where)
+    _call_on(device, stream, lib().grouped_matmul_dw, (C.byref(g), dy.data_ptr(), x.data_ptr(), out.data_ptr(),
+                                                       _code_of(out, where), alpha, beta, ws.data_ptr(), ws.numel()), where)
     return out
 
 
@@ -638,10 +645,8 @@ class StackStep:
     def __call__(self, stream=None) -> None:
         if not self.stacks:
             return
-        dev, s = _call_stream(self.stacks[0].W, stream)
-        with dev:
-            _check(lib().muon_stack_step(self._table, len(self.stacks), C.byref(self.params), _ptr(self.ws), self.ws.numel(),
-                                         s), "muon_stack_step")
+        _call_on(self.stacks[0].W.get_device(), stream, lib().muon_stack_step,
+                 (self._table, len(self.stacks), C.byref(self.params), _ptr(self.ws), self.ws.numel()), "muon_stack_step")
 
     def accumulate(self, i: int, dy, x, offsets, stream=None) -> None:
         """M <- mu M + dy_e^T x_e for the experts of stack i, whose G is None:

@@ -291,3 +291,45 @@ def test_gradients_against_differences(cuda):
         if grad is dx:
             tol += 2.0 ** -11 * (dx.double().abs() * delta[0].abs()).sum().item()
         assert abs(loss(*a) - loss(*b) - slope) <= 1.01 * tol
+
+
+def test_long_sums_keep_fp32(cuda):
+    """Thousands of rows in one expert: parts of 512 rows, each losing at most 2^-24 of its running sum in each of its
+    32 instructions. A sum of random signs grows like a square root, so the running sum is 2/3 of the part's on
+    average, and a truncation loses half a step on average: 32 * 2^-24 * 2/3 * 1/2 of the part, and less than that of
+    the whole once parts add up: below 2^-20. The additions of parts are rounded to nearest, 2^-24 each."""
+    d = torch.bfloat16
+    c = [5000, 1024, 1025, 3, 2049]
+    total = sum(c)
+    off = offsets_of(c)
+    x, dy = draw((total, 72), 1.0, d, 1), draw((total, 264), 1.0, d, 2)
+    old = draw((5, 264, 72), 1.0, torch.float32, 3)
+    for beta in (0.0, 0.95):
+        dw = old.clone()
+        mu.grouped_matmul_dw(dy, x, off, out=dw, beta=beta)
+        want, _ = dw_ref(dy, x, off, 1.0, beta, old)
+        for e in range(5):
+            assert (dw[e].double() - want[e]).norm() <= 2.0 ** -20 * want[e].norm()
+
+
+def test_short_device_wait_is_reported(cuda):
+    """A wait bound of nothing: every role stops, copies and products in flight are drained, the context stays usable."""
+    d = torch.bfloat16
+    off = offsets_of([300, 212])
+    x, w, dy = draw((512, 8192), 1.0, d, 1), draw((2, 512, 8192), 0.02, d, 2), draw((512, 512), 1.0, d, 3)
+    calls = (lambda st: mu.grouped_matmul(x, w, off, dev_status=st), lambda st: mu.grouped_matmul_dx(dy, w, off, dev_status=st),
+             lambda st: mu.grouped_matmul_dw(dy, x, off, dev_status=st))
+    for call in calls:
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        mu.set_wait_timeout_ns(1)
+        try:
+            call(status)
+            torch.cuda.synchronize()
+        finally:
+            mu.set_wait_timeout_ns(0)
+        assert int(status.item()) == mu.ERR_TIMEOUT
+        status.zero_()
+        call(status)
+        assert int(status.item()) == mu.OK
+    for r, want, mag in rows_ref(x, w, off, True):
+        close(mu.grouped_matmul(x, w, off)[r], want, mag, 8192, d)
