@@ -1043,6 +1043,12 @@ muon_status check_stacks(const muon_stack* st, int32_t count, const muon_stack_p
   return MUON_OK;
 }
 
+// Small matrices are updated by one launch with the matrix on chip, which
+// needs no workspace; the rest by row kernels and the chain of products.
+bool resident(const muon_stack& k, const muon_ns_params* ns, Op t) {
+  return t != Op::F32 && !ns->gram && resident_fits(k.rows, k.cols);
+}
+
 struct StackPlan {
   struct Grp {
     int stack;
@@ -1050,6 +1056,7 @@ struct StackPlan {
     size_t row_base, mat_base;
   };
   std::vector<Grp> groups;
+  std::vector<int> small;
   size_t scale, xscale, rsum, ctr, total;
 };
 
@@ -1058,6 +1065,10 @@ StackPlan plan_stacks(const muon_stack* st, int32_t count, const muon_ns_params*
   size_t rows = 0, mats = 0;
   for (int i = 0; i < count; ++i) {
     if (empty_stack(st[i])) continue;
+    if (resident(st[i], ns, t)) {
+      q.small.push_back(i);
+      continue;
+    }
     q.groups.push_back(StackPlan::Grp{i, {}, rows, mats});
     rows += (size_t)st[i].count * st[i].rows;
     mats += (size_t)st[i].count;
@@ -1112,7 +1123,7 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
   muon_ns_params ns = p->ns;
   if (planes == 2) ns.compute = MUON_F16;
   const StackPlan q = plan_stacks(st, count, &ns, t, planes);
-  if (q.groups.empty()) return MUON_OK;
+  if (q.groups.empty() && q.small.empty()) return MUON_OK;
   if (!ws) return MUON_ERR_WORKSPACE;
   if (!aligned16(ws)) return MUON_ERR_ALIGN;
   if (ws_bytes < q.total) return MUON_ERR_WORKSPACE;
@@ -1123,44 +1134,57 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
   // Frobenius scale enters the first products; the others are scaled once
   // the norm is known.
   const bool folded = planes == 1 && t == Op::BF16;
-  std::vector<NsGroup> groups;
-  std::vector<StackLaunch> launches((q.groups.size() + kMaxStacks - 1) / kMaxStacks);
-  for (size_t gi = 0; gi < q.groups.size(); ++gi) {
-    const StackPlan::Grp& g = q.groups[gi];
-    const muon_stack& k = st[g.stack];
-    const int64_t n = k.rows < k.cols ? k.rows : k.cols, m = k.rows < k.cols ? k.cols : k.rows;
-    StackLaunch& L = launches[gi / kMaxStacks];
-    if (gi % kMaxStacks == 0) {
-      memset(&L, 0, sizeof(L));
-      L.rsum = at<double>(ws, q.rsum) + g.row_base;
-      L.scale = at<float>(ws, q.scale) + g.mat_base;
-      L.xscale = at<float>(ws, q.xscale) + g.mat_base;
-      L.mu = p->mu;
-      L.step = p->lr * p->scale;
-      L.keep = 1.f - p->lr * p->weight_decay;
-      L.eps = ns.norm_eps;
-      L.nesterov = p->nesterov;
-      L.folded = folded;
-      L.status = status;
-    }
+  StackLaunch proto;
+  memset(&proto, 0, sizeof(proto));
+  proto.mu = p->mu;
+  proto.step = p->lr * p->scale;
+  proto.keep = 1.f - p->lr * p->weight_decay;
+  proto.eps = ns.norm_eps;
+  proto.nesterov = p->nesterov;
+  proto.folded = folded;
+  proto.status = status;
+  auto add = [](StackLaunch& L, const muon_stack& k) -> StackMat& {
     StackMat& e = L.m[L.count++];
     e.W = k.W; e.w_stride = k.w_stride; e.w_ld = k.w_ld; e.w_type = k.w_dtype;
     e.M = k.M; e.m_stride = k.m_stride; e.m_ld = k.m_ld;
     e.G = k.G; e.g_stride = k.g_stride; e.g_ld = k.g_ld; e.g_type = k.g_dtype;
     e.copy = k.copy; e.c_stride = k.copy_stride; e.c_ld = k.copy_ld; e.c_type = k.copy_dtype;
-    e.X = at<void>(ws, g.b.X[0]);
     e.ldx = pad_ld(k.cols);
     e.rows = (int32_t)k.rows; e.cols = (int32_t)k.cols; e.count = (int32_t)k.count;
     e.row_begin = L.total_rows;
     e.mat_begin = L.total_mats;
     L.total_rows += (int)(k.count * k.rows);
     L.total_mats += (int)k.count;
-    e.kappa = planes == 2 ? pow2_near(std::sqrt((double)n * m), 16384.0) : folded ? 1.f : kappa_for(t, n);
     auto four = [](const void* ptr, int64_t es, int64_t ld, int64_t stride) {
       return !ptr || (reinterpret_cast<uintptr_t>(ptr) % (uintptr_t)(4 * es) == 0 && ld % 4 == 0 && stride % 4 == 0);
     };
     e.vec = k.cols % 4 == 0 && four(k.W, bytes_of(k.w_dtype), k.w_ld, k.w_stride) && four(k.M, 4, k.m_ld, k.m_stride) &&
             four(k.G, k.G ? bytes_of(k.g_dtype) : 4, k.g_ld, k.g_stride) && four(k.copy, 2, k.copy_ld, k.copy_stride);
+    return e;
+  };
+  auto kappa_of = [](const muon_stack& k) { return pow2_near(std::sqrt((double)k.rows * (double)k.cols), 16384.0); };
+  auto rho_of = [](const muon_stack& k) { return pow2_near((double)(k.rows < k.cols ? k.rows : k.cols), 4096.0); };
+
+  for (int i : q.small) {
+    StackLaunch L = proto;
+    add(L, st[i]);
+    TRY(launch_stack_resident(L, ns, t, planes, kappa_of(st[i]), rho_of(st[i]), timeout_ns(), s));
+  }
+  std::vector<NsGroup> groups;
+  std::vector<StackLaunch> launches((q.groups.size() + kMaxStacks - 1) / kMaxStacks, proto);
+  for (size_t gi = 0; gi < q.groups.size(); ++gi) {
+    const StackPlan::Grp& g = q.groups[gi];
+    const muon_stack& k = st[g.stack];
+    const int64_t n = k.rows < k.cols ? k.rows : k.cols;
+    StackLaunch& L = launches[gi / kMaxStacks];
+    if (L.count == 0) {
+      L.rsum = at<double>(ws, q.rsum) + g.row_base;
+      L.scale = at<float>(ws, q.scale) + g.mat_base;
+      L.xscale = at<float>(ws, q.xscale) + g.mat_base;
+    }
+    StackMat& e = add(L, k);
+    e.X = at<void>(ws, g.b.X[0]);
+    e.kappa = planes == 2 ? kappa_of(k) : folded ? 1.f : kappa_for(t, n);
 
     NsGroup ng{};
     ng.rows = k.rows;
@@ -1170,7 +1194,7 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
     ng.X[1] = at<void>(ws, g.b.X[1]);
     ng.xscale = at<float>(ws, q.xscale) + g.mat_base;
     for (int i = 0; i < (planes == 2 ? 2 : ns_work_buffers(&ns)); ++i) ng.nb[i] = at<void>(ws, g.b.nb[i]);
-    ng.rho = planes == 2 ? pow2_near((double)n, 4096.0) : rho_for(t, n);
+    ng.rho = planes == 2 ? rho_of(k) : rho_for(t, n);
     ng.part = g.b.part_bytes ? at<float>(ws, g.b.part) : nullptr;
     ng.part_bytes = g.b.part_bytes;
     ng.planes = planes;

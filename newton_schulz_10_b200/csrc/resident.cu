@@ -1,0 +1,637 @@
+// The whole update of a stack of small matrices in one launch: momentum,
+// norm, Newton-Schulz chain and weight update with the matrix resident on
+// chip. For matrices whose shorter side n is at most 128 and whose longer
+// side m at most 2048.
+//
+// The chain of a small matrix is bound by latency: 15 dependent products of a
+// few microseconds each, every one paying a launch, its setup, a pipeline
+// fill and a drain. Here a cluster of C CTAs (1, 2, 4 or 8) holds one matrix:
+// CTA r keeps columns [r mc, (r+1) mc) of the wide view X (n x m) in shared
+// memory, mc = 64 g <= 256, as operands of tcgen05.mma; per step
+//   A  = sum over the cluster of X_r X_r^T   (M = 128, N = n, K = mc)
+//   B' = a I + b A + c A A                   (every CTA, K = n)
+//   X_r <- B' X_r                            (N = mc, K = n)
+// where the sum goes through distributed shared memory: each CTA adds its
+// share of the rows over the partial results of all, in rank order, and
+// writes the operand to every CTA. Folding a X into B' saves reading X back
+// in the epilogue.
+//
+// A and B' always keep two planes (hi + lo of the operand type): they never
+// leave the chip, and with one plane the rounding of their diagonals would be
+// the largest error of the chain (a 513 x 33 bf16 matrix, whose singular
+// values are all alike: 2.6e-2 with one plane). X has one plane in bf16 and
+// fp16 and two in two-plane fp16.
+//
+// Both products that read X use the same copy of it: 64-column groups of
+// 128-byte rows with 128-byte swizzle are K-major for X X^T and MN-major for
+// B' X. Rows n.. of the M side may hold anything (they only reach accumulator
+// lanes that are never read), but the K side of B' X reads rows up to np, n
+// rounded up to 16, which are zero.
+//
+// Until the norm is known, and for the last step's result, an element's fp32
+// value is kept split over the two planes' places (its high and low 16 bits),
+// so neither needs memory of its own.
+//
+// A product of two-plane operands is hi hi + hi lo + lo hi, as in the
+// Newton-Schulz GEMM; X is stored times kappa and A, B' times rho, powers of
+// two.
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+#include "common.cuh"
+#include "rowio.cuh"
+#include "stack.cuh"
+
+namespace muon {
+
+namespace res {
+
+constexpr int THREADS = 256;
+constexpr int WARPS = THREADS / 32;
+constexpr int MAX_N = 128;      // rows of the wide view
+constexpr int MAX_G = 4;        // 64-column groups per CTA
+constexpr int MAX_C = 8;        // CTAs per cluster
+constexpr int GROUP = 128 * 128;  // bytes of one 64-column group of one plane
+constexpr int A_BYTES = 4 * GROUP;  // two groups of two planes; also 128 x 128 fp32 partial sums
+constexpr int MISC = 1024;
+constexpr int TMEM_COLS = 512;
+constexpr uint64_t DRAIN_NS = 1000000000ull;
+constexpr int X_COL = 128;      // TMEM column of X's accumulator (A's is 0)
+
+constexpr int smem_bytes(int g) {
+  // one CTA per SM: two would wait for each other's TMEM columns
+  const int b = 1024 + 2 * g * GROUP + A_BYTES + MISC;
+  return b > 120 * 1024 ? b : 120 * 1024;
+}
+static_assert(smem_bytes(MAX_G) <= 232448, "exceeds the opt-in shared memory of one sm_100 CTA");
+
+struct Params {
+  StackMat m;
+  int n, np, long_side, tall;  // wide view: n x long_side
+  int g, C;
+  float mu, step, keep, eps;
+  int nesterov, T;
+  float kappa, rho;
+  float coeffs[MUON_MAX_T][3];
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u2(uint32_t a, uint2 v) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f64(uint32_t a, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+}
+// generic-proxy writes to shared memory (this CTA's and its peers') before the tensor core reads them
+__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
+  const uint32_t addr = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(addr, parity)) {
+    if (globaltimer_ns() - t0 > DRAIN_NS) {
+      report(status, MUON_ERR_TIMEOUT);
+      break;
+    }
+  }
+}
+
+// Byte offset of 16-byte chunk ch (8 columns) of row r in a 64-column group.
+__device__ __forceinline__ uint32_t at(int r, int ch) { return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4)); }
+
+// Eight values to operand chunks: the high plane at hi, the low one at lo.
+template <typename T, int PL>
+__device__ __forceinline__ void put8(uint8_t* hi, uint8_t* lo, const float* v) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = Elem<T>::pack2(v[2 * i], v[2 * i + 1]);
+    if (PL == 2) {
+      const float2 f = Elem<T>::unpack2(h[i]);
+      l[i] = Elem<T>::pack2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+    }
+  }
+  *reinterpret_cast<uint4*>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (PL == 2) *reinterpret_cast<uint4*>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+template <typename T, int PL>
+__device__ __forceinline__ void get8(const uint8_t* hi, const uint8_t* lo, float* v) {
+  const uint4 h = *reinterpret_cast<const uint4*>(hi);
+  const uint32_t hh[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Elem<T>::unpack2(hh[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+  if (PL == 2) {
+    const uint4 l = *reinterpret_cast<const uint4*>(lo);
+    const uint32_t ll[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = Elem<T>::unpack2(ll[i]);
+      v[2 * i] += f.x;
+      v[2 * i + 1] += f.y;
+    }
+  }
+}
+// Eight fp32 values as their high and low halves in the two planes' places.
+__device__ __forceinline__ void put8_raw(uint8_t* hi, uint8_t* lo, const float* v) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
+    h[i] = __byte_perm(a, b, 0x7632);
+    l[i] = __byte_perm(a, b, 0x5410);
+  }
+  *reinterpret_cast<uint4*>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint4*>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+__device__ __forceinline__ void get8_raw(const uint8_t* hi, const uint8_t* lo, float* v) {
+  const uint4 h = *reinterpret_cast<const uint4*>(hi), l = *reinterpret_cast<const uint4*>(lo);
+  const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(__byte_perm(ll[i], hh[i], 0x5410));
+    v[2 * i + 1] = __uint_as_float(__byte_perm(ll[i], hh[i], 0x7632));
+  }
+}
+
+template <typename T, int PL>
+__global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int g = p.g, C = p.C;
+  uint8_t* const X = smem;                     // high plane: g groups; low plane behind
+  uint8_t* const Xl = X + g * GROUP;
+  uint8_t* const A = X + 2 * g * GROUP;        // high plane: two groups; low plane behind
+  uint8_t* const Al = A + 2 * GROUP;
+  double* slots = reinterpret_cast<double*>(A + A_BYTES);  // one partial norm per CTA of the cluster
+  double* scratch = slots + MAX_C;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(scratch + 32);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = C > 1 ? (int)cluster_rank() : 0;
+  const int mat = (int)blockIdx.x / C;
+  auto sync_all = [&]() {
+    if (C > 1) cluster_sync(); else __syncthreads();
+  };
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  // rows 0..np of every group: zeros where the matrix has no element
+  for (int i = tid; i < 2 * g * p.np * 8; i += THREADS) {
+    const int grp = i / (p.np * 8), rest = i - grp * p.np * 8;
+    *reinterpret_cast<uint4*>(X + grp * GROUP + rest * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  tc_fence_before();
+  sync_all();  // also: every CTA of the cluster has started, so its shared memory may be written
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_dependents_launch();
+
+  // ------------------------------------------------------------------
+  // momentum and the update's target, in fp32 halves
+  // ------------------------------------------------------------------
+  const StackMat& m = p.m;
+  const int mc = 64 * g;
+  const int first = rank * mc;  // this CTA's columns of the wide view
+  const int width = max(0, min(mc, p.long_side - first));
+  float* const M = m.M + (int64_t)mat * m.m_stride;
+  const void* const G = m.G ? row_at(m.G, m.g_type, (int64_t)mat * m.g_stride) : nullptr;
+  void* const W = row_at(m.W, m.w_type, (int64_t)mat * m.w_stride);
+  void* const K = m.copy ? row_at(m.copy, m.c_type, (int64_t)mat * m.c_stride) : nullptr;
+  // stored rows of this CTA and the contiguous run in each of them
+  const int srows = p.tall ? width : p.n, srow0 = p.tall ? first : 0;
+  const int scols = p.tall ? p.n : width, scol0 = p.tall ? 0 : first;
+  // byte offset (within a plane) of stored element (r, c) of this CTA
+  auto spot = [&](int r, int c) -> uint32_t {
+    const int i = p.tall ? c : r, j = p.tall ? r : c;
+    return (uint32_t)((j >> 6) * GROUP) + at(i, (j & 63) >> 3) + (j & 7) * 2;
+  };
+  auto put_raw = [&](int r, int c, float v) {
+    const uint32_t o = spot(r, c), u = __float_as_uint(v);
+    *reinterpret_cast<uint16_t*>(X + o) = (uint16_t)(u >> 16);
+    *reinterpret_cast<uint16_t*>(Xl + o) = (uint16_t)u;
+  };
+  auto get_raw = [&](int r, int c) -> float {
+    const uint32_t o = spot(r, c);
+    return __uint_as_float(((uint32_t)*reinterpret_cast<const uint16_t*>(X + o) << 16) |
+                           *reinterpret_cast<const uint16_t*>(Xl + o));
+  };
+  double ss = 0.0;
+  if (m.vec) {
+    constexpr int U = 4;  // rows in flight per warp
+    for (int r0 = warp; r0 < srows; r0 += WARPS * U) {
+      for (int c = 4 * lane; c < scols; c += 128) {
+        float4 y[U], gr[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r < srows) {
+            y[u] = *reinterpret_cast<const float4*>(M + (srow0 + r) * m.m_ld + scol0 + c);
+            if (G) gr[u] = load4(row_at(G, m.g_type, (srow0 + r) * m.g_ld + scol0), m.g_type, c);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r >= srows) break;
+          float4 v = y[u];
+          if (G) {
+            v.x = fmaf(p.mu, v.x, gr[u].x); v.y = fmaf(p.mu, v.y, gr[u].y);
+            v.z = fmaf(p.mu, v.z, gr[u].z); v.w = fmaf(p.mu, v.w, gr[u].w);
+            *reinterpret_cast<float4*>(M + (srow0 + r) * m.m_ld + scol0 + c) = v;
+            v.x = target(v.x, gr[u].x, p.mu, p.nesterov); v.y = target(v.y, gr[u].y, p.mu, p.nesterov);
+            v.z = target(v.z, gr[u].z, p.mu, p.nesterov); v.w = target(v.w, gr[u].w, p.mu, p.nesterov);
+          }
+          if (p.tall) {
+            put_raw(r, c, v.x); put_raw(r, c + 1, v.y); put_raw(r, c + 2, v.z); put_raw(r, c + 3, v.w);
+          } else {
+            const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y), d = __float_as_uint(v.z),
+                           e = __float_as_uint(v.w);
+            const uint32_t o = spot(r, c);
+            *reinterpret_cast<uint2*>(X + o) = make_uint2(__byte_perm(a, b, 0x7632), __byte_perm(d, e, 0x7632));
+            *reinterpret_cast<uint2*>(Xl + o) = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(d, e, 0x5410));
+          }
+          const double a = v.x, b = v.y, d = v.z, e = v.w;
+          ss += a * a + b * b + d * d + e * e;
+        }
+      }
+    }
+  } else {
+    for (int r = warp; r < srows; r += WARPS)
+      for (int c = lane; c < scols; c += 32) {
+        float* q = M + (srow0 + r) * m.m_ld + scol0 + c;
+        float v = *q;
+        if (G) {
+          const float gr = load1(row_at(G, m.g_type, (srow0 + r) * m.g_ld + scol0), m.g_type, c);
+          v = fmaf(p.mu, v, gr);
+          *q = v;
+          v = target(v, gr, p.mu, p.nesterov);
+        }
+        put_raw(r, c, v);
+        ss += (double)v * (double)v;
+      }
+  }
+  double total = block_sum(ss, scratch);
+  if (C > 1) {
+    if (tid < C) st_cluster_f64(mapa_shared(smem_u32(slots + rank), (uint32_t)tid), total);
+    cluster_sync();
+    total = 0.0;
+    for (int r = 0; r < C; ++r) total += slots[r];  // in rank order: the same sum in every CTA
+  }
+  if (!isfinite(total) && tid == 0 && rank == 0) report(p.status, MUON_ERR_NONFINITE);
+  const double inv = total > 0.0 ? 1.0 / (sqrt(total) + (double)p.eps) : 0.0;
+  const float sc = inv > 3.4028234663852886e38 ? 3.4028234663852886e38f : (float)inv;
+  __syncthreads();  // every element is in place
+  for (int i = tid; i < g * p.np * 8; i += THREADS) {
+    const int grp = i / (p.np * 8), rest = i - grp * p.np * 8;
+    uint8_t* h = X + grp * GROUP + rest * 16;
+    float v[8];
+    get8_raw(h, h + g * GROUP, v);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = v[x] * sc * p.kappa;
+    put8<T, PL>(h, h + g * GROUP, v);
+  }
+
+  // ------------------------------------------------------------------
+  // the chain
+  // ------------------------------------------------------------------
+  constexpr int fmt = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+  // Descriptors hold 14 bits of the address; in a cluster the bits above the
+  // shared-memory window carry the CTA's rank and must not reach the other fields.
+  const uint32_t a_a = smem_u32(A);
+  const uint32_t x_d = smem_u32(X) & 0x3FFFFu, a_d = a_a & 0x3FFFFu;
+  const uint32_t x_low = PL == 2 ? (uint32_t)(g * GROUP) >> 4 : 0u, a_low = (uint32_t)(2 * GROUP) >> 4;
+  const uint64_t k_major = smem_desc_sw128(0, 16, 1024);       // 8-row groups 1 KB apart
+  const uint64_t mn_major = smem_desc_sw128(0, GROUP, 1024);   // 64-column atoms 16 KB apart
+  const uint32_t idesc_n = idesc_f16(fmt, 0, 0, 128, p.np), idesc_x = idesc_f16(fmt, 0, 1, 128, mc);
+  uint32_t parity = 0;
+  // after the operands are written: order them before the products, which
+  // thread 0 issues, and wait for their completion. A wait that runs out
+  // reports it and then still waits, with the drain's bound, so that nothing
+  // reads, overwrites or frees what a product in flight uses; the cluster's
+  // barriers need every CTA, so the chain goes on.
+  auto products = [&](auto issue) {
+    fence_operands();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      issue();
+      umma_commit(bar);
+    }
+    if (!mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, p.status)) drain_wait(bar, parity, p.status);
+    parity ^= 1;
+    __syncwarp();
+    tc_fence_after();
+  };
+  // hi hi, + hi lo where the N side has two planes, + lo hi where the M side has
+  auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t low_a, uint32_t low_b, uint32_t idesc, bool acc) {
+    umma_f16(d, ad, bd, idesc, acc);
+    if (low_b) umma_f16(d, ad, bd + low_b, idesc, 1);
+    if (low_a) umma_f16(d, ad + low_a, bd, idesc, 1);
+  };
+  const int q = warp & 3, half = warp >> 2;
+  const int row = q * 32 + lane;                 // this thread's accumulator lane
+  const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+  const bool rows_here = q * 32 < p.np;          // warp-uniform
+
+  for (int t = 0; t < p.T; ++t) {
+    const float a = p.coeffs[t][0], b = p.coeffs[t][1], c = p.coeffs[t][2];
+    // A = X X^T over this CTA's columns
+    products([&]() {
+      for (int j = 0; j < g; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t d = k_major | (uint64_t)((x_d + j * GROUP + k * 32) >> 4);
+          mma(tmem, d, d, x_low, x_low, idesc_n, j != 0 || k != 0);
+        }
+    });
+    const float alpha = p.rho / (p.kappa * p.kappa);
+    if (C == 1) {
+      if (rows_here)
+        for (int c0 = half * 16; c0 < p.np; c0 += 32) {
+          uint32_t r[16];
+          tmem_ld_32x16(tl + c0, r);
+          tmem_wait_ld();
+          float v[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] = alpha * __uint_as_float(r[x]);
+          const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t w = o + at(row, ((c0 & 63) >> 3) + s);
+            put8<T, 2>(A + w, Al + w, v + 8 * s);
+          }
+        }
+    } else {
+      // partial sums in fp32 where A's planes go (B' of the last step has
+      // been read): rows of 512 bytes, 16-byte chunks swizzled by the row
+      if (rows_here)
+        for (int c0 = half * 16; c0 < p.np; c0 += 32) {
+          uint32_t r[16];
+          tmem_ld_32x16(tl + c0, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            *reinterpret_cast<uint4*>(A + row * 512 + ((((c0 >> 2) + s) ^ (row & 31)) << 4)) =
+                make_uint4(r[4 * s], r[4 * s + 1], r[4 * s + 2], r[4 * s + 3]);
+        }
+      tc_fence_before();
+      cluster_sync();
+      // CTA r sums rows r, r + C, ... over the cluster, four columns a thread
+      constexpr int MAXV = 128 / 2 * 32 / THREADS;
+      float4 v[MAXV];
+      const int cpr = p.np >> 2;  // chunks per row
+      const int mine = (p.np - rank + C - 1) / C * cpr;
+#pragma unroll
+      for (int s = 0; s < MAXV; ++s) {
+        const int i = tid + s * THREADS;
+        if (i >= mine) break;
+        const int r = rank + C * (i / cpr), ch = i % cpr;
+        const uint32_t o = a_a + r * 512 + ((ch ^ (r & 31)) << 4);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < C; ++k) {
+          const float4 x = ld_cluster_f4(mapa_shared(o, (uint32_t)k));
+          sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+        }
+        v[s] = make_float4(alpha * sum.x, alpha * sum.y, alpha * sum.z, alpha * sum.w);
+      }
+      cluster_sync();  // every partial sum has been read
+#pragma unroll
+      for (int s = 0; s < MAXV; ++s) {
+        const int i = tid + s * THREADS;
+        if (i >= mine) break;
+        const int r = rank + C * (i / cpr), c0 = 4 * (i % cpr);
+        const uint2 h = pack4<T>(v[s]);
+        const float4 f = unpack4((const T*)nullptr, h);
+        const uint2 l = pack4<T>(make_float4(v[s].x - f.x, v[s].y - f.y, v[s].z - f.z, v[s].w - f.w));
+        const uint32_t o = a_a + (c0 >> 6) * GROUP + at(r, (c0 & 63) >> 3) + (c0 & 7) * 2;
+        for (int k = 0; k < C; ++k) {
+          const uint32_t d = mapa_shared(o, (uint32_t)k);
+          st_cluster_u2(d, h);
+          st_cluster_u2(d + 2 * GROUP, l);
+        }
+      }
+      fence_operands();
+      cluster_sync();
+    }
+    // B' = a I + b A + c A A, in A's place (every thread rewrites what it read)
+    products([&]() {
+      for (int k = 0; k < p.np / 16; ++k) {
+        const uint64_t d = k_major | (uint64_t)((a_d + (k >> 2) * GROUP + (k & 3) * 32) >> 4);
+        mma(tmem, d, d, a_low, a_low, idesc_n, k != 0);
+      }
+    });
+    if (rows_here)
+      for (int c0 = half * 16; c0 < p.np; c0 += 32) {
+        uint32_t r[16];
+        tmem_ld_32x16(tl + c0, r);
+        tmem_wait_ld();
+        const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t w = o + at(row, ((c0 & 63) >> 3) + s);
+          float v[8];
+          get8<T, 2>(A + w, Al + w, v);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            v[x] = fmaf(c / p.rho, __uint_as_float(r[8 * s + x]), b * v[x]);
+            if (c0 + 8 * s + x == row) v[x] += p.rho * a;
+          }
+          put8<T, 2>(A + w, Al + w, v);
+        }
+      }
+    // X <- B' X
+    products([&]() {
+      for (int k = 0; k < p.np / 16; ++k) {
+        const uint64_t ad = k_major | (uint64_t)((a_d + (k >> 2) * GROUP + (k & 3) * 32) >> 4);
+        const uint64_t bd = mn_major | (uint64_t)((x_d + k * 2048) >> 4);
+        mma(tmem + X_COL, ad, bd, a_low, x_low, idesc_x, k != 0);
+      }
+    });
+    const bool last = t + 1 == p.T;
+    const float back = last ? 1.f / (p.rho * p.kappa) : 1.f / p.rho;
+    if (rows_here)
+      for (int c0 = half * 32; c0 < mc; c0 += 64) {
+        uint32_t r[32];
+        tmem_ld_32x32(tl + X_COL + c0, r);
+        tmem_wait_ld();
+        if (row < p.np) {
+          const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            float v[8];
+            const uint32_t w = o + at(row, ((c0 & 63) >> 3) + s);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] = back * __uint_as_float(r[8 * s + x]);
+            if (last) put8_raw(X + w, Xl + w, v);
+            else put8<T, PL>(X + w, Xl + w, v);
+          }
+        }
+      }
+  }
+  tc_fence_before();
+  sync_all();  // the result is in place; no peer writes here any more
+
+  // ------------------------------------------------------------------
+  // W <- keep W - step O
+  // ------------------------------------------------------------------
+  bool bad = false;
+  if (m.vec) {
+    constexpr int U = 4;
+    for (int r0 = warp; r0 < srows; r0 += WARPS * U) {
+      for (int c = 4 * lane; c < scols; c += 128) {
+        float4 w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r < srows) w[u] = load4(row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0), m.w_type, c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r >= srows) break;
+          float4 o;
+          if (p.tall) {
+            o = make_float4(get_raw(r, c), get_raw(r, c + 1), get_raw(r, c + 2), get_raw(r, c + 3));
+          } else {
+            const uint32_t s = spot(r, c);
+            const uint2 h = *reinterpret_cast<const uint2*>(X + s), l = *reinterpret_cast<const uint2*>(Xl + s);
+            o = make_float4(__uint_as_float(__byte_perm(l.x, h.x, 0x5410)), __uint_as_float(__byte_perm(l.x, h.x, 0x7632)),
+                            __uint_as_float(__byte_perm(l.y, h.y, 0x5410)), __uint_as_float(__byte_perm(l.y, h.y, 0x7632)));
+          }
+          bad |= !(isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w));
+          float4 v = w[u];
+          v.x = fmaf(-p.step, o.x, p.keep * v.x); v.y = fmaf(-p.step, o.y, p.keep * v.y);
+          v.z = fmaf(-p.step, o.z, p.keep * v.z); v.w = fmaf(-p.step, o.w, p.keep * v.w);
+          store4(row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0), m.w_type, c, v);
+          if (K) store4(row_at(K, m.c_type, (srow0 + r) * m.c_ld + scol0), m.c_type, c, v);
+        }
+      }
+    }
+  } else {
+    for (int r = warp; r < srows; r += WARPS)
+      for (int c = lane; c < scols; c += 32) {
+        const float o = get_raw(r, c);
+        bad |= !isfinite(o);
+        void* wr = row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0);
+        const float v = fmaf(-p.step, o, p.keep * load1(wr, m.w_type, c));
+        store1(wr, m.w_type, c, v);
+        if (K) store1(row_at(K, m.c_type, (srow0 + r) * m.c_ld + scol0), m.c_type, c, v);
+      }
+  }
+  if (bad) report(p.status, MUON_ERR_NONFINITE);
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+}  // namespace res
+
+namespace {
+
+template <typename T, int PL>
+muon_status launch_resident(const res::Params& p, cudaStream_t s) {
+  static std::mutex mu;
+  static bool ready[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(res::stack_resident<T, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               res::smem_bytes(res::MAX_G)) != cudaSuccess) {
+        cudaGetLastError();
+        return MUON_ERR_CUDA;
+      }
+      ready[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.m.count * p.C));
+  cfg.blockDim = dim3(res::THREADS);
+  cfg.dynamicSmemBytes = res::smem_bytes(p.g);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.C > 1 ? 2 : 1;
+  counters().launches += 1;
+  return cudaLaunchKernelEx(&cfg, res::stack_resident<T, PL>, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+}  // namespace
+
+bool resident_fits(int64_t rows, int64_t cols) {
+  return std::min(rows, cols) <= res::MAX_N && std::max(rows, cols) <= (int64_t)res::MAX_C * 64 * res::MAX_G;
+}
+
+muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns, Op t, int planes, float kappa, float rho,
+                                  uint64_t timeout_ns, cudaStream_t s) {
+  res::Params p{};
+  p.m = L.m[0];
+  p.tall = p.m.rows > p.m.cols;
+  p.n = p.tall ? p.m.cols : p.m.rows;
+  p.long_side = p.tall ? p.m.rows : p.m.cols;
+  p.np = (p.n + 15) / 16 * 16;
+  // The smallest cluster that holds the matrix; a larger one while the GPU
+  // has SMs to spare, since half the columns a CTA halve two of the three
+  // products.
+  const int groups = (p.long_side + 63) / 64;
+  p.C = 1;
+  while ((groups + p.C - 1) / p.C > res::MAX_G) p.C *= 2;
+  while (p.C < res::MAX_C && (groups + p.C - 1) / p.C > 1 && (int64_t)p.m.count * p.C * 2 <= num_sms()) p.C *= 2;
+  p.g = (groups + p.C - 1) / p.C;
+  p.mu = L.mu;
+  p.step = L.step;
+  p.keep = L.keep;
+  p.eps = L.eps;
+  p.nesterov = L.nesterov;
+  p.T = ns.T;
+  p.kappa = kappa;
+  p.rho = rho;
+  for (int i = 0; i < ns.T; ++i)
+    for (int j = 0; j < 3; ++j) p.coeffs[i][j] = ns.coeffs[i][j];
+  p.status = L.status;
+  p.timeout_ns = timeout_ns;
+  if (planes == 2) return launch_resident<__half, 2>(p, s);
+  return t == Op::BF16 ? launch_resident<__nv_bfloat16, 1>(p, s) : launch_resident<__half, 1>(p, s);
+}
+
+}  // namespace muon
