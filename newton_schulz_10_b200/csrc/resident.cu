@@ -5,15 +5,18 @@
 //
 // The chain of a small matrix is bound by latency: 15 dependent products of a
 // few microseconds each, every one paying a launch, its setup, a pipeline
-// fill and a drain. Here a cluster of C CTAs (1, 2, 4 or 8) holds one matrix:
+// fill and a drain. Here a cluster of C CTAs (1 to 16) holds one matrix:
 // CTA r keeps columns [r mc, (r+1) mc) of the wide view X (n x m) in shared
 // memory, mc = 64 g <= 256, as operands of tcgen05.mma; per step
 //   A  = sum over the cluster of X_r X_r^T   (M = 128, N = n, K = mc)
 //   B' = a I + b A + c A A                   (every CTA, K = n)
 //   X_r <- B' X_r                            (N = mc, K = n)
-// where the sum goes through distributed shared memory: each CTA adds its
-// share of the rows over the partial results of all, in rank order, and
-// writes the operand to every CTA. Folding a X into B' saves reading X back
+// where the sum goes through distributed shared memory by bulk copies: CTA r
+// receives its np / C rows of every partial result, adds them in rank order
+// and copies its rows of the operand to every CTA. Both arrive on mbarriers,
+// so the loop has no cluster barrier; that copies may land is implied by what
+// has arrived (below). Element-wise remote stores took 1500 to 5900 cycles a
+// step where these take a few hundred. Folding a X into B' saves reading X back
 // in the epilogue.
 //
 // A and B' always keep two planes (hi + lo of the operand type): they never
@@ -50,21 +53,25 @@ namespace res {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_N = 128;      // rows of the wide view
+constexpr int MAX_M = 2048;     // columns of the wide view
 constexpr int MAX_G = 4;        // 64-column groups per CTA
-constexpr int MAX_C = 8;        // CTAs per cluster
+constexpr int MAX_C = 16;       // CTAs per cluster (above 8 only where a smaller one cannot hold the matrix)
 constexpr int GROUP = 128 * 128;  // bytes of one 64-column group of one plane
-constexpr int A_BYTES = 4 * GROUP;  // two groups of two planes; also 128 x 128 fp32 partial sums
 constexpr int MISC = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr uint64_t DRAIN_NS = 1000000000ull;
 constexpr int X_COL = 128;      // TMEM column of X's accumulator (A's is 0)
 
-constexpr int smem_bytes(int g) {
-  // one CTA per SM: two would wait for each other's TMEM columns
-  const int b = 1024 + 2 * g * GROUP + A_BYTES + MISC;
+constexpr int SMEM_MAX = 232448;  // opt-in shared memory of one sm_100 CTA
+
+// X (g groups) and A (np rows and columns), two planes each, and with a
+// cluster the np x np fp32 sums. At least 120 KB, so that an SM holds one CTA
+// (two would wait for each other's TMEM columns).
+constexpr int smem_bytes(int g, int np, int C) {
+  const int b = 1024 + 2 * g * GROUP + 2 * ((np + 63) / 64) * GROUP + (C > 1 ? np * np * 4 : 0) + MISC;
   return b > 120 * 1024 ? b : 120 * 1024;
 }
-static_assert(smem_bytes(MAX_G) <= 232448, "exceeds the opt-in shared memory of one sm_100 CTA");
+static_assert(smem_bytes(MAX_G, MAX_N, 1) <= SMEM_MAX && smem_bytes(2, MAX_N, MAX_C) <= SMEM_MAX, "every shape fits");
 
 struct Params {
   StackMat m;
@@ -72,28 +79,31 @@ struct Params {
   int g, C;
   float mu, step, keep, eps;
   int nesterov, T;
-  float kappa, rho;
-  float coeffs[MUON_MAX_T][3];
+  float kappa;
+  float alpha;            // rho / kappa^2: the stored A from X X^T
+  float back, last;       // 1 / rho, and 1 / (rho kappa) for the last step's result
+  float lin[MUON_MAX_T], quad[MUON_MAX_T], diag[MUON_MAX_T];  // b, c / rho, rho a: the stored B'
   int* status;
   unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
+// Copy of `bytes` of this CTA's shared memory to a CTA of the cluster (its own
+// included), whose barrier counts the bytes.
+__device__ __forceinline__ void copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
                : "memory");
-  return v;
 }
-__device__ __forceinline__ void st_cluster_u2(uint32_t a, uint2 v) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+// Arrive on a barrier of another CTA, ordered after this thread's earlier accesses.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void st_cluster_f64(uint32_t a, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
 }
-// generic-proxy writes to shared memory (this CTA's and its peers') before the tensor core reads them
-__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
+// generic-proxy accesses to this CTA's shared memory before the tensor core or a bulk copy touches it
+__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -183,12 +193,16 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   const int g = p.g, C = p.C;
   uint8_t* const X = smem;                     // high plane: g groups; low plane behind
   uint8_t* const Xl = X + g * GROUP;
-  uint8_t* const A = X + 2 * g * GROUP;        // high plane: two groups; low plane behind
-  uint8_t* const Al = A + 2 * GROUP;
-  double* slots = reinterpret_cast<double*>(A + A_BYTES);  // one partial norm per CTA of the cluster
+  uint8_t* const A = X + 2 * g * GROUP;        // high plane; low plane behind
+  const int a_plane = (p.np + 63) / 64 * GROUP;
+  uint8_t* const Al = A + a_plane;
+  uint8_t* const R = Al + a_plane;  // cluster: partial sums of this CTA's rows, [C][np / C][np] fp32
+  double* slots = reinterpret_cast<double*>(R + (C > 1 ? p.np * p.np * 4 : 0));  // one partial norm per CTA of the cluster
   double* scratch = slots + MAX_C;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(scratch + 32);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(scratch + 32);  // products done
+  uint64_t* sums = bar + 1;   // partial sums arrived, and every CTA's own have been sent
+  uint64_t* rows = bar + 2;   // rows of A arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -200,6 +214,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
 
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(sums, (uint32_t)C + 1);
+    mbar_init(rows, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -250,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   };
   double ss = 0.0;
   if (m.vec) {
-    constexpr int U = 4;  // rows in flight per warp
+    constexpr int U = 8;  // rows in flight per warp
     for (int r0 = warp; r0 < srows; r0 += WARPS * U) {
       for (int c = 4 * lane; c < scols; c += 128) {
         float4 y[U], gr[U];
@@ -260,6 +276,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
           if (r < srows) {
             y[u] = *reinterpret_cast<const float4*>(M + (srow0 + r) * m.m_ld + scol0 + c);
             if (G) gr[u] = load4(row_at(G, m.g_type, (srow0 + r) * m.g_ld + scol0), m.g_type, c);
+            // W is read at the end: into L2 meanwhile
+            prefetch_l2(row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0 + c));
           }
         }
 #pragma unroll
@@ -332,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   // shared-memory window carry the CTA's rank and must not reach the other fields.
   const uint32_t a_a = smem_u32(A);
   const uint32_t x_d = smem_u32(X) & 0x3FFFFu, a_d = a_a & 0x3FFFFu;
-  const uint32_t x_low = PL == 2 ? (uint32_t)(g * GROUP) >> 4 : 0u, a_low = (uint32_t)(2 * GROUP) >> 4;
+  const uint32_t x_low = PL == 2 ? (uint32_t)(g * GROUP) >> 4 : 0u, a_low = (uint32_t)a_plane >> 4;
   const uint64_t k_major = smem_desc_sw128(0, 16, 1024);       // 8-row groups 1 KB apart
   const uint64_t mn_major = smem_desc_sw128(0, GROUP, 1024);   // 64-column atoms 16 KB apart
   const uint32_t idesc_n = idesc_f16(fmt, 0, 0, 128, p.np), idesc_x = idesc_f16(fmt, 0, 1, 128, mc);
@@ -342,6 +360,9 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   // reports it and then still waits, with the drain's bound, so that nothing
   // reads, overwrites or frees what a product in flight uses; the cluster's
   // barriers need every CTA, so the chain goes on.
+  auto wait_for = [&](uint64_t* b, uint32_t par) {
+    if (!mbar_wait_bounded(b, par, abort_flag, p.timeout_ns, p.status)) drain_wait(b, par, p.status);
+  };
   auto products = [&](auto issue) {
     fence_operands();
     tc_fence_before();
@@ -351,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       issue();
       umma_commit(bar);
     }
-    if (!mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, p.status)) drain_wait(bar, parity, p.status);
+    wait_for(bar, parity);
     parity ^= 1;
     __syncwarp();
     tc_fence_after();
@@ -366,9 +387,25 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   const int row = q * 32 + lane;                 // this thread's accumulator lane
   const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
   const bool rows_here = q * 32 < p.np;          // warp-uniform
+  const int swz = p.np % 32 == 0 ? 7 : 3;        // 16-byte chunks of the fp32 sums, swizzled by the row
+  const int rows_per = p.np / C;                 // rows of A that this CTA sums (np is a multiple of 16)
+  // This thread's columns of A's accumulator, 16 from half * 16, half * 16 +
+  // 32, ...: all loads in flight before the one wait. Returns their count.
+  auto load_chunks = [&](float (&v)[4][16]) -> int {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (half * 16 + 32 * k < p.np) {  // warp-uniform
+        tmem_ld_32x16(tl + half * 16 + 32 * k, reinterpret_cast<uint32_t(&)[16]>(v[k]));
+        n = k + 1;
+      }
+    tmem_wait_ld();
+    return n;
+  };
 
   for (int t = 0; t < p.T; ++t) {
-    const float a = p.coeffs[t][0], b = p.coeffs[t][1], c = p.coeffs[t][2];
+    const float lin = p.lin[t], quad = p.quad[t], diag = p.diag[t], alpha = p.alpha;
+    const uint32_t odd = (uint32_t)t & 1u;  // phase of the exchange's barriers
     // A = X X^T over this CTA's columns
     products([&]() {
       for (int j = 0; j < g; ++j)
@@ -378,74 +415,89 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
           mma(tmem, d, d, x_low, x_low, idesc_n, j != 0 || k != 0);
         }
     });
-    const float alpha = p.rho / (p.kappa * p.kappa);
-    if (C == 1) {
-      if (rows_here)
-        for (int c0 = half * 16; c0 < p.np; c0 += 32) {
-          uint32_t r[16];
-          tmem_ld_32x16(tl + c0, r);
-          tmem_wait_ld();
-          float v[16];
+    if (rows_here) {
+      float v[4][16];
+      const int chunks = load_chunks(v);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] = alpha * __uint_as_float(r[x]);
+      for (int k = 0; k < 4; ++k) {
+        if (k >= chunks) break;
+        const int c0 = half * 16 + 32 * k;
+        if (C == 1) {
           const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[k][x] *= alpha;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const uint32_t w = o + at(row, ((c0 & 63) >> 3) + s);
-            put8<T, 2>(A + w, Al + w, v + 8 * s);
+            put8<T, 2>(A + w, Al + w, v[k] + 8 * s);
           }
-        }
-    } else {
-      // partial sums in fp32 where A's planes go (B' of the last step has
-      // been read): rows of 512 bytes, 16-byte chunks swizzled by the row
-      if (rows_here)
-        for (int c0 = half * 16; c0 < p.np; c0 += 32) {
-          uint32_t r[16];
-          tmem_ld_32x16(tl + c0, r);
-          tmem_wait_ld();
+        } else if (row < p.np) {
+          // partial sums in fp32 where A's planes go: B' of the last step has
+          // been read, and the peers send rows of A only once this CTA's
+          // partial sums have left
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            *reinterpret_cast<uint4*>(A + row * 512 + ((((c0 >> 2) + s) ^ (row & 31)) << 4)) =
-                make_uint4(r[4 * s], r[4 * s + 1], r[4 * s + 2], r[4 * s + 3]);
+            *reinterpret_cast<float4*>(A + row * p.np * 4 + ((((c0 >> 2) + s) ^ (row & swz)) << 4)) =
+                make_float4(v[k][4 * s], v[k][4 * s + 1], v[k][4 * s + 2], v[k][4 * s + 3]);
         }
-      tc_fence_before();
-      cluster_sync();
-      // CTA r sums rows r, r + C, ... over the cluster, four columns a thread
-      constexpr int MAXV = 128 / 2 * 32 / THREADS;
-      float4 v[MAXV];
-      const int cpr = p.np >> 2;  // chunks per row
-      const int mine = (p.np - rank + C - 1) / C * cpr;
-#pragma unroll
-      for (int s = 0; s < MAXV; ++s) {
-        const int i = tid + s * THREADS;
-        if (i >= mine) break;
-        const int r = rank + C * (i / cpr), ch = i % cpr;
-        const uint32_t o = a_a + r * 512 + ((ch ^ (r & 31)) << 4);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < C; ++k) {
-          const float4 x = ld_cluster_f4(mapa_shared(o, (uint32_t)k));
-          sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
-        }
-        v[s] = make_float4(alpha * sum.x, alpha * sum.y, alpha * sum.z, alpha * sum.w);
       }
-      cluster_sync();  // every partial sum has been read
-#pragma unroll
-      for (int s = 0; s < MAXV; ++s) {
-        const int i = tid + s * THREADS;
-        if (i >= mine) break;
-        const int r = rank + C * (i / cpr), c0 = 4 * (i % cpr);
-        const uint2 h = pack4<T>(v[s]);
-        const float4 f = unpack4((const T*)nullptr, h);
-        const uint2 l = pack4<T>(make_float4(v[s].x - f.x, v[s].y - f.y, v[s].z - f.z, v[s].w - f.w));
-        const uint32_t o = a_a + (c0 >> 6) * GROUP + at(r, (c0 & 63) >> 3) + (c0 & 7) * 2;
-        for (int k = 0; k < C; ++k) {
-          const uint32_t d = mapa_shared(o, (uint32_t)k);
-          st_cluster_u2(d, h);
-          st_cluster_u2(d + 2 * GROUP, l);
+    }
+    if (C > 1) {
+      const uint32_t part = (uint32_t)(rows_per * p.np * 4);
+      fence_operands();
+      tc_fence_before();
+      __syncthreads();
+      if (warp == 0) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(sums, part * C);
+          mbar_arrive_expect_tx(rows, (uint32_t)(2 * a_plane / GROUP * p.np * 128));
         }
+        __syncwarp();
+        if (lane < C) {
+          // rows lane * rows_per .. to that CTA, in its slot for this one. It
+          // has added what came in the last step: rows of A from it followed.
+          copy_cluster(mapa_shared(smem_u32(R) + rank * part, (uint32_t)lane), a_a + lane * part, part,
+                       mapa_shared(smem_u32(sums), (uint32_t)lane));
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        __syncwarp();  // all of this CTA's copies have been read: its A may be overwritten
+        if (lane < C) arrive_cluster(mapa_shared(smem_u32(sums), (uint32_t)lane));
+      }
+      wait_for(sums, odd);
+      // the sums of this CTA's rows, eight columns a thread, at their place
+      const int cpr = p.np >> 3;
+      for (int j = tid; j < rows_per * cpr; j += THREADS) {
+        const int lr = j / cpr, c0 = 8 * (j - lr * cpr);
+        float v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < C; ++k) {
+          const uint8_t* src = R + (k * rows_per + lr) * p.np * 4;
+          const int x0 = (rank * rows_per + lr) & swz, ch = c0 >> 2;
+          const float4 x = *reinterpret_cast<const float4*>(src + ((ch ^ x0) << 4));
+          const float4 y = *reinterpret_cast<const float4*>(src + (((ch + 1) ^ x0) << 4));
+          v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+          v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] *= alpha;
+        const uint32_t w = (uint32_t)((c0 >> 6) * GROUP) + at(rank * rows_per + lr, (c0 & 63) >> 3);
+        put8<T, 2>(A + w, Al + w, v);
       }
       fence_operands();
-      cluster_sync();
+      __syncthreads();
+      // and to the peers: every CTA's partial sums have left its A
+      const int pieces = 2 * a_plane / GROUP;  // groups of both planes, contiguous
+      for (int i = tid; i < pieces * C; i += THREADS) {
+        const int to = i / pieces;
+        if (to == rank) continue;
+        const uint32_t o = a_a + (i - to * pieces) * GROUP + rank * rows_per * 128;
+        copy_cluster(mapa_shared(o, (uint32_t)to), o, (uint32_t)(rows_per * 128), mapa_shared(smem_u32(rows), (uint32_t)to));
+      }
+      if (tid == 0) mbar_complete_tx(rows, (uint32_t)(pieces * rows_per * 128));  // its own are there
+      wait_for(rows, odd);
     }
     // B' = a I + b A + c A A, in A's place (every thread rewrites what it read)
     products([&]() {
@@ -454,11 +506,13 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
         mma(tmem, d, d, a_low, a_low, idesc_n, k != 0);
       }
     });
-    if (rows_here)
-      for (int c0 = half * 16; c0 < p.np; c0 += 32) {
-        uint32_t r[16];
-        tmem_ld_32x16(tl + c0, r);
-        tmem_wait_ld();
+    if (rows_here) {
+      float y[4][16];
+      const int chunks = load_chunks(y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= chunks) break;
+        const int c0 = half * 16 + 32 * k;
         const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -467,12 +521,13 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
           get8<T, 2>(A + w, Al + w, v);
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
-            v[x] = fmaf(c / p.rho, __uint_as_float(r[8 * s + x]), b * v[x]);
-            if (c0 + 8 * s + x == row) v[x] += p.rho * a;
+            v[x] = fmaf(quad, y[k][8 * s + x], lin * v[x]);
+            if (c0 + 8 * s + x == row) v[x] += diag;
           }
           put8<T, 2>(A + w, Al + w, v);
         }
       }
+    }
     // X <- B' X
     products([&]() {
       for (int k = 0; k < p.np / 16; ++k) {
@@ -482,9 +537,9 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       }
     });
     const bool last = t + 1 == p.T;
-    const float back = last ? 1.f / (p.rho * p.kappa) : 1.f / p.rho;
+    const float back = last ? p.last : p.back;
     if (rows_here)
-      for (int c0 = half * 32; c0 < mc; c0 += 64) {
+      for (int c0 = half * 32; c0 < mc; c0 += 64) {  // one group an iteration
         uint32_t r[32];
         tmem_ld_32x32(tl + X_COL + c0, r);
         tmem_wait_ld();
@@ -510,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   // ------------------------------------------------------------------
   bool bad = false;
   if (m.vec) {
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int r0 = warp; r0 < srows; r0 += WARPS * U) {
       for (int c = 4 * lane; c < scols; c += 128) {
         float4 w[U];
@@ -571,7 +626,8 @@ muon_status launch_resident(const res::Params& p, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
       if (cudaFuncSetAttribute(res::stack_resident<T, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               res::smem_bytes(res::MAX_G)) != cudaSuccess) {
+                               res::SMEM_MAX) != cudaSuccess ||
+          cudaFuncSetAttribute(res::stack_resident<T, PL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
         cudaGetLastError();
         return MUON_ERR_CUDA;
       }
@@ -581,7 +637,7 @@ muon_status launch_resident(const res::Params& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.m.count * p.C));
   cfg.blockDim = dim3(res::THREADS);
-  cfg.dynamicSmemBytes = res::smem_bytes(p.g);
+  cfg.dynamicSmemBytes = res::smem_bytes(p.g, p.np, p.C);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -599,7 +655,7 @@ muon_status launch_resident(const res::Params& p, cudaStream_t s) {
 }  // namespace
 
 bool resident_fits(int64_t rows, int64_t cols) {
-  return std::min(rows, cols) <= res::MAX_N && std::max(rows, cols) <= (int64_t)res::MAX_C * 64 * res::MAX_G;
+  return std::min(rows, cols) <= res::MAX_N && std::max(rows, cols) <= res::MAX_M;
 }
 
 muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns, Op t, int planes, float kappa, float rho,
@@ -614,10 +670,11 @@ muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns
   // has SMs to spare, since half the columns a CTA halve two of the three
   // products.
   const int groups = (p.long_side + 63) / 64;
+  auto per_cta = [&](int C) { return (groups + C - 1) / C; };
   p.C = 1;
-  while ((groups + p.C - 1) / p.C > res::MAX_G) p.C *= 2;
-  while (p.C < res::MAX_C && (groups + p.C - 1) / p.C > 1 && (int64_t)p.m.count * p.C * 2 <= num_sms()) p.C *= 2;
-  p.g = (groups + p.C - 1) / p.C;
+  while (per_cta(p.C) > res::MAX_G || res::smem_bytes(per_cta(p.C), p.np, p.C) > res::SMEM_MAX) p.C *= 2;
+  while (p.C < 8 && per_cta(p.C) > 1 && (int64_t)p.m.count * p.C * 2 <= num_sms()) p.C *= 2;
+  p.g = per_cta(p.C);
   p.mu = L.mu;
   p.step = L.step;
   p.keep = L.keep;
@@ -625,9 +682,14 @@ muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns
   p.nesterov = L.nesterov;
   p.T = ns.T;
   p.kappa = kappa;
-  p.rho = rho;
-  for (int i = 0; i < ns.T; ++i)
-    for (int j = 0; j < 3; ++j) p.coeffs[i][j] = ns.coeffs[i][j];
+  p.alpha = rho / kappa / kappa;
+  p.back = 1.f / rho;
+  p.last = 1.f / rho / kappa;
+  for (int i = 0; i < ns.T; ++i) {
+    p.lin[i] = ns.coeffs[i][1];
+    p.quad[i] = ns.coeffs[i][2] / rho;
+    p.diag[i] = ns.coeffs[i][0] * rho;
+  }
   p.status = L.status;
   p.timeout_ns = timeout_ns;
   if (planes == 2) return launch_resident<__half, 2>(p, s);
