@@ -39,7 +39,9 @@
 // partial buffer, then split_reduce_kernel sums the parts in a fixed order,
 // applies the epilogue and writes both triangles, so the result is
 // deterministic and exactly symmetric) or, when not split, runs on
-// 128-column tiles if they all fit in one wave.
+// 128-column tiles if they all fit in one wave. Two-plane launches that fit
+// take 128x64 tiles on single CTAs instead: twice to four times the tiles,
+// each with half the epilogue.
 //
 // Two planes (PL = 2, fp16): a matrix is the sum of two fp16 planes, hi =
 // fp16(x) and lo = fp16(x - hi), 22 bits of x, stored as matrices 2b and
@@ -72,6 +74,7 @@ namespace tc {
 constexpr int BM = 128, BK = 64;  // BM: rows per CTA
 constexpr int BN_WIDE = 256;      // tile columns: 256, or 128 for launches too small to fill the GPU
 constexpr int BN_NARROW = 128;
+constexpr int BN_SMALL = 64;      // two planes only: single CTAs, for launches of a few tiles
 constexpr int UMMA_K = 16;
 constexpr int EPI_WARP0 = 4;
 constexpr int EPI_WARPS = 8;                       // two per TMEM lane quarter
@@ -85,7 +88,7 @@ constexpr uint64_t DRAIN_NS = 1000000000ull;
 
 template <int PAIR, int BN, int PL = 1>
 struct Cfg {
-  static constexpr int STAGES = (PAIR == 2 ? (BN == BN_WIDE ? 6 : 8) : (BN == BN_WIDE ? 4 : 6)) / PL;
+  static constexpr int STAGES = (PAIR == 2 ? (BN == BN_WIDE ? 6 : 8) : (BN == BN_WIDE ? 4 : BN == BN_NARROW ? 6 : 8)) / PL;
   static constexpr int A_STAGE = BM * BK * 2 * PL;             // this CTA's 128 rows of A (all planes)
   static constexpr int B_STAGE = (BN / PAIR) * BK * 2 * PL;    // this CTA's share of B's BN rows
   static constexpr int EPI_CHUNKS = BN / 32 / 2;               // 32-column chunks per epilogue warp
@@ -1287,8 +1290,8 @@ void count_job(const tc::Job& g, int tile_m, int bn, int planes = 1) {
 
 muon_status tc_gemm(Op t, const GemmDesc* gd, int ngroups, int* status, uint64_t timeout_ns, cudaStream_t s) {
   if (ngroups < 1 || ngroups > kMaxGemmGroups || (t != Op::BF16 && t != Op::F16)) return MUON_ERR_INVALID_ARG;
-  const int pair = g_pair_mode;
-  const int tile_m = tc::BM * pair;
+  int pair = g_pair_mode;
+  int tile_m = tc::BM * pair;
   const int planes = gd[0].planes == 2 ? 2 : 1;  // the same for every group of a launch
   if (planes == 2 && t != Op::F16) return MUON_ERR_INVALID_ARG;
   int units = units_for<tc::BN_WIDE>(t, pair, planes);
@@ -1334,6 +1337,20 @@ muon_status tc_gemm(Op t, const GemmDesc* gd, int ngroups, int* status, uint64_t
     if (total_narrow > total_wide && total_narrow <= units_narrow) {
       bn = tc::BN_NARROW;
       units = units_narrow;
+    }
+    if (planes == 2) {
+      // 15 dependent launches of a few tiles each are bound by a tile's own
+      // latency: the smallest tile wins while all fit in one wave
+      int total_small = 0;
+      for (int i = 0; i < ng; ++i) total_small += desc_tiles(*src[i], tc::BM, tc::BN_SMALL) * src[i]->batch;
+      const int units_small = max_units<__half, 1, tc::BN_SMALL, 2>();
+      if (units_small <= 0) return MUON_ERR_CUDA;
+      if (total_small <= units_small) {
+        bn = tc::BN_SMALL;
+        units = units_small;
+        pair = 1;
+        tile_m = tc::BM;
+      }
     }
   }
 
@@ -1393,8 +1410,9 @@ muon_status tc_gemm(Op t, const GemmDesc* gd, int ngroups, int* status, uint64_t
   cn.launches += sp.ngroups ? 2 : 1;
   cn.gemm_launches += 1;
   for (int i = 0; i < ng; ++i) count_job(p.g[i], tile_m, bn, planes);
-  const muon_status r = bn == tc::BN_WIDE ? launch_for<tc::BN_WIDE>(t, pair, p, total, units, s, planes)
-                                          : launch_for<tc::BN_NARROW>(t, pair, p, total, units, s, planes);
+  const muon_status r = bn == tc::BN_WIDE     ? launch_for<tc::BN_WIDE>(t, pair, p, total, units, s, planes)
+                        : bn == tc::BN_NARROW ? launch_for<tc::BN_NARROW>(t, pair, p, total, units, s, planes)
+                                              : launch<__half, 1, tc::BN_SMALL, 2>(p, total, units, s);
   if (r != MUON_OK || sp.ngroups == 0) return r;
   return t == Op::BF16 ? launch_reduce<__nv_bfloat16>(sp, red_blocks, s) : launch_reduce<__half>(sp, red_blocks, s);
 }

@@ -30,8 +30,9 @@ struct Shape {
 
 // Two planes (NsGroup::planes = 2): X is kept as kappa X and A, B as rho A,
 // rho B, so that both planes stay in fp16's normal range; the constants enter
-// the epilogues:  A <- (rho / kappa^2) X X^T,  B <- (c / rho) A A + b A,
-// X <- (1 / rho) B X + a X.
+// the epilogues:  A <- (rho / kappa^2) X X^T,  B <- (c / rho) A A + b A + rho a I,
+// X <- (1 / rho) B X. With 22 bits a X can go through B's diagonal, which saves
+// the largest product both planes of its C operand.
 
 Shape shape_of(const NsGroup& g) {
   Shape s;
@@ -157,11 +158,11 @@ muon_status run_standard(const Launcher& L, NsGroup* gs, int ng, const muon_ns_p
     TRY(L(d, ng));
     for (int i = 0; i < ng; ++i)
       d[i] = sym_of(gs[i], gs[i].nb[0], gs[i].nb[0], gs[i].nb[1], gs[i].nb[0], gs[i].planes == 2 ? c / gs[i].rho : c, b,
-                    0.f);
+                    gs[i].planes == 2 ? gs[i].rho * a : 0.f);
     TRY(L(d, ng));
     for (int i = 0; i < ng; ++i) {
       NsGroup& g = gs[i];
-      d[i] = g.planes == 2 ? apply_of(g, g.nb[1], g.X[g.cur], g.X[g.cur ^ 1], 1.f / g.rho, a, nullptr, 0, 0)
+      d[i] = g.planes == 2 ? apply_of(g, g.nb[1], g.X[g.cur], g.X[g.cur ^ 1], 1.f / g.rho, 0.f, nullptr, 0, 0)
                            : apply_of(g, g.nb[1], g.X[g.cur], g.X[g.cur ^ 1], 1.f, a, first ? g.xscale : nullptr, 1, 1);
     }
     TRY(L(d, ng));
