@@ -390,7 +390,9 @@ muon_status grouped_matmul(const muon_grouped* g, const void* x, const void* w, 
 /* dx[r,:] = dy[r,:] W_e: the gradient of grouped_matmul for its rows. */
 muon_status grouped_matmul_dx(const muon_grouped* g, const void* dy, const void* w, void* dx, void* stream);
 
-/* Workspace bytes of grouped_matmul_dw (0 if experts is out of range). */
+/* Workspace bytes of grouped_matmul_dw (0 if experts is out of range): about
+ * 20 MB, for sums of parts of an expert's rows when there are few tiles. Query
+ * with the device that will run the call current. */
 size_t grouped_workspace_size(int32_t experts);
 
 /* dW_e = alpha sum_r dy[r,:]^T x[r,:] + beta dW_e over the rows r of expert e:

@@ -28,10 +28,14 @@
 // per expert, copies of the two operands' tensor maps whose row count ends
 // with the expert's last row, so that the copies themselves fill zeros behind
 // it. An expert without rows gets beta dW_e (0 when beta is 0).
+// When there are fewer tiles than CTA pairs, each expert's rows are cut into
+// parts, one work unit each, whose fp32 sums go to the workspace (at most one
+// per CTA pair); a second launch adds them in order.
 //
 // Every wait is bounded as in the Newton-Schulz GEMM; offsets are clamped to
 // 0..tokens before use, and a decreasing or out-of-range entry is reported as
 // MUON_ERR_INVALID_ARG.
+#include <algorithm>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -85,7 +89,8 @@ struct Params {
   int tokens, experts;
   int M, N, K;            // ROWS: M = features out, K = features in; DW: M = n, N = k
   int a_mn;               // ROWS: W read MN-major
-  int vec;                // DW: 16-byte accesses of out are aligned
+  int splits;             // DW: parts of an expert's rows (1: none, results go to out)
+  float* partial;         // DW, splits > 1: 256 x 256 fp32 per (tile, part)
   float alpha, beta;      // DW
   int* status;
   unsigned long long timeout_ns;
@@ -109,8 +114,9 @@ struct Tile {
   int n0;        // ROWS: first token; DW: first column of the pair's N side
   int nvalid;    // ROWS: tokens of this tile
   int n_mma;     // N of the instruction
-  int t0, t1;    // DW: the expert's rows (the K side)
+  int t0;        // DW: first row of the K side
   int nkb;       // k-blocks
+  bool whole;    // DW: the tile's only part
 };
 
 // Token tiles of a group of `cnt` rows, and their width: equal shares of a
@@ -144,20 +150,26 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* tile_begin, i
     const int left = s.end - t.n0;
     t.nvalid = left < w ? left : w;
     t.n_mma = (t.nvalid + 31) & ~31;
-    t.t0 = t.t1 = 0;
+    t.t0 = 0;
     t.nkb = (p.K + BK - 1) / BK;
+    t.whole = true;
   } else {
-    const int per = mt * ntl;
-    t.e = tile / per;
-    const int r = tile - t.e * per;
+    const int per = mt * ntl, u = tile / p.splits;
+    t.e = u / per;
+    const int r = u - t.e * per;
     t.m0 = (r / ntl) * TILE_M;
     t.n0 = (r % ntl) * NT;
     t.nvalid = 0;
     t.n_mma = NT;
     const Span s = span_of(p, t.e);
     t.t0 = s.begin;
-    t.t1 = s.end;
     t.nkb = (s.end - s.begin + BK - 1) / BK;
+    t.whole = p.splits == 1;
+    if (!t.whole) {
+      const int each = (t.nkb + p.splits - 1) / p.splits, first = (tile - u * p.splits) * each;
+      t.t0 += first * BK;
+      t.nkb = max(0, min(each, t.nkb - first));
+    }
   }
   return t;
 }
@@ -363,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     }
     total = all * mt;
   } else {
-    total = p.experts * mt * ntl;
+    total = p.experts * mt * ntl * p.splits;
   }
   tc_fence_before();
   __syncwarp();
@@ -554,27 +566,77 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         }
       } else {
         // block: lanes = rows of dW_e, columns = its columns; staged so that
-        // eight lanes cover a row of 32 consecutive elements
-        O* const out = reinterpret_cast<O*>(p.out) + (long long)t.e * p.so;
+        // neighbouring lanes hold neighbouring columns. A part of a tile goes
+        // to its 256 x 256 place in the workspace (none when it has no rows).
+        const bool skip = !t.whole && t.nkb == 0;
+        O* const out = t.whole ? reinterpret_cast<O*>(p.out) + (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0
+                               : reinterpret_cast<O*>(p.partial) + (long long)tile * (TILE_M * NT);
+        const long long ldo = t.whole ? p.ldo : NT;
+        const int rows = skip ? 0 : min(p.M - r0, 32), wr = r0 - t.m0;  // rows of this warp, from row wr of the tile
         for (int c = half * 32; c < NT; c += 64) {
-          const int c0 = t.n0 + c;
-          if (r0 >= p.M || c0 >= p.N) break;  // warp-uniform
-          const int cc = c0 + (lane & 7) * 4;
+          const int cols = p.N - t.n0 - c;
+          if (rows <= 0 || cols <= 0) break;  // warp-uniform
+          if (t.nkb == 0 && beta == 0.f) {
+            constexpr int V = 16 / sizeof(O);  // no rows, nothing to add to: zeros
+            for (int i = lane; i < rows * (32 / V); i += 32) {
+              const int r = i / (32 / V), x0 = (i % (32 / V)) * V;
+              O* d = out + (wr + r) * ldo + c + x0;
+              if (x0 + V <= cols) *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
+              else
+                for (int x = 0; x < V; ++x)
+                  if (x0 + x < cols) d[x] = f_to_out<O>(0.f);
+            }
+            continue;
+          }
+          if (!std::is_same<O, float>::value && beta == 0.f) {
+            // 16-bit result alone: rounded before it is staged, four lanes a row
+            uint32_t raw[32];
+            tmem_ld_32x32(trow + c, raw);
+            tmem_wait_ld();
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t h[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                h[x] = Elem<T>::pack2(p.alpha * __uint_as_float(raw[8 * k + 2 * x]), p.alpha * __uint_as_float(raw[8 * k + 2 * x + 1]));
+              *reinterpret_cast<uint4*>(sd + sw64(lane, 8 * k)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            __syncwarp();
+            const int x0 = (lane & 3) * 8;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = 8 * j + (lane >> 2);
+              if (r >= rows || x0 >= cols) continue;
+              const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(r, x0));
+              O* d = out + (wr + r) * ldo + c + x0;
+              if (x0 + 8 <= cols) {
+                *reinterpret_cast<uint4*>(d) = v;
+              } else {
+                const O* h = reinterpret_cast<const O*>(&v);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  if (x0 + x < cols) d[x] = h[x];
+              }
+            }
+            continue;
+          }
+          const int cc = (lane & 7) * 4;
+          O* const at = out + (wr + (lane >> 3)) * ldo + c + cc;  // row 4 j + lane / 8 at at + 4 j ldo
           float4 old[8];
           if (beta != 0.f) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const int r = r0 + 4 * j + (lane >> 3);
               old[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (r >= p.M || cc >= p.N) continue;
-              const O* d = out + (long long)r * p.ldo + cc;
-              if (p.vec && cc + 4 <= p.N) {
+              if (4 * j + (lane >> 3) >= rows || cc >= cols) continue;
+              const O* d = at + 4 * j * ldo;
+              if (cc + 4 <= cols) {
                 old[j] = load_out4<O>(d);
               } else {
                 float* o = &old[j].x;
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                  if (cc + x < p.N) o[x] = out_to_f<O>(d[x]);
+                  if (cc + x < cols) o[x] = out_to_f<O>(d[x]);
               }
             }
           }
@@ -595,22 +657,21 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int rr = 4 * j + (lane >> 3);
-            const int r = r0 + rr;
-            if (r >= p.M || cc >= p.N) continue;
+            if (rr >= rows || cc >= cols) continue;
             float4 v = *reinterpret_cast<const float4*>(sd + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
             v.x *= p.alpha; v.y *= p.alpha; v.z *= p.alpha; v.w *= p.alpha;
             if (beta != 0.f) {
               v.x = fmaf(beta, old[j].x, v.x); v.y = fmaf(beta, old[j].y, v.y);
               v.z = fmaf(beta, old[j].z, v.z); v.w = fmaf(beta, old[j].w, v.w);
             }
-            O* d = out + (long long)r * p.ldo + cc;
-            if (p.vec && cc + 4 <= p.N) {
+            O* d = at + 4 * j * ldo;
+            if (cc + 4 <= cols) {
               store_out4<O>(d, v);
             } else {
               const float* o = &v.x;
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                if (cc + x < p.N) d[x] = f_to_out<O>(o[x]);
+                if (cc + x < cols) d[x] = f_to_out<O>(o[x]);
             }
           }
         }
@@ -637,6 +698,41 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
   __syncwarp();
   cluster_sync();
   if (warp == 2) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+// dW = alpha sum of the parts + beta dW: four columns a thread, parts in order.
+template <typename O>
+__global__ void __launch_bounds__(256) add_parts(const __grid_constant__ Params p) {
+  grid_dependency_wait();
+  const int q = (p.N + 3) / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)p.experts * p.M * q) return;
+  const int c = (int)(i % q) * 4;
+  const long long er = i / q;
+  const int e = (int)(er / p.M), r = (int)(er % p.M);
+  const Span s = span_of(p, e);
+  const int nkb = (s.end - s.begin + BK - 1) / BK, each = (nkb + p.splits - 1) / p.splits;
+  const int mt = (p.M + TILE_M - 1) / TILE_M, ntl = (p.N + 255) / 256;
+  const long long tile = ((long long)e * mt + r / TILE_M) * ntl + c / 256;
+  const float* src = p.partial + tile * p.splits * (TILE_M * 256) + (r % TILE_M) * 256 + c % 256;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k * each < nkb; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(src + (long long)k * (TILE_M * 256));
+    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+  }
+  v.x *= p.alpha; v.y *= p.alpha; v.z *= p.alpha; v.w *= p.alpha;
+  O* d = reinterpret_cast<O*>(p.out) + (long long)e * p.so + (long long)r * p.ldo + c;
+  if (c + 4 <= p.N) {
+    if (p.beta != 0.f) {
+      const float4 o = load_out4<O>(d);
+      v.x = fmaf(p.beta, o.x, v.x); v.y = fmaf(p.beta, o.y, v.y); v.z = fmaf(p.beta, o.z, v.z); v.w = fmaf(p.beta, o.w, v.w);
+    }
+    store_out4<O>(d, v);
+  } else {
+    const float* y = &v.x;
+    for (int x = 0; c + x < p.N; ++x) d[x] = f_to_out<O>(p.beta != 0.f ? fmaf(p.beta, out_to_f<O>(d[x]), y[x]) : y[x]);
+  }
 }
 
 }  // namespace grp
@@ -685,7 +781,7 @@ int pair_units() {
 }
 
 template <typename T, typename O, int MODE, int NT>
-muon_status launch_grouped(const grp::Params& p, long long tiles, cudaStream_t s) {
+muon_status launch_grouped(const grp::Params& p, long long tiles, cudaStream_t s) {  // tiles: at most, to size the grid
   const int units = pair_units<T, O, MODE, NT>();
   if (units <= 0) return MUON_ERR_CUDA;
   const int use = tiles < units ? (int)tiles : units;
@@ -719,11 +815,11 @@ muon_status rows_typed(grp::Params& p, int nt, cudaStream_t s) {
   }
 }
 
-template <typename T, typename O>
-muon_status dw_typed(const grp::Params& p, cudaStream_t s) {
-  const int threads = 128, blocks = (2 * p.experts + threads - 1) / threads;
+// A small launch that may start while the one before it ends.
+template <typename F>
+muon_status launch_plain(F* kernel, long long blocks, int threads, const grp::Params& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -732,9 +828,32 @@ muon_status dw_typed(const grp::Params& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   counters().launches += 1;
-  if (cudaLaunchKernelEx(&cfg, grp::clip_maps, p) != cudaSuccess) return MUON_ERR_CUDA;
-  const long long mt = (p.M + grp::TILE_M - 1) / grp::TILE_M, nt = (p.N + 255) / 256;
-  return launch_grouped<T, O, grp::DW, 256>(p, mt * nt * p.experts, s);
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+}
+
+// A part of an expert's rows pays for its fp32 sum's way through memory and
+// the second launch from about 4 k-blocks (256 rows) on.
+constexpr int kMinPartBlocks = 4;
+constexpr int kMaxParts = 16;
+
+template <typename T, typename O>
+muon_status dw_typed(grp::Params& p, cudaStream_t s) {
+  muon_status r = launch_plain(grp::clip_maps, (2 * p.experts + 127) / 128, 128, p, s);
+  if (r != MUON_OK) return r;
+  const long long mt = (p.M + grp::TILE_M - 1) / grp::TILE_M, nt = (p.N + 255) / 256, tiles = mt * nt * p.experts;
+  const int units = pair_units<T, float, grp::DW, 256>();
+  if (units <= 0) return MUON_ERR_CUDA;
+  long long parts = units / tiles;
+  parts = std::min(parts, (long long)p.tokens / p.experts / (64 * kMinPartBlocks));
+  p.splits = (int)std::max(1ll, std::min(parts, (long long)kMaxParts));
+  if (p.splits == 1) return launch_grouped<T, O, grp::DW, 256>(p, tiles, s);
+  grp::Params q = p;
+  q.alpha = 1.f;
+  q.beta = 0.f;
+  r = launch_grouped<T, float, grp::DW, 256>(q, tiles * p.splits, s);
+  if (r != MUON_OK) return r;
+  const long long quads = (long long)p.experts * p.M * ((p.N + 3) / 4);
+  return launch_plain(grp::add_parts<O>, (quads + 255) / 256, 256, p, s);
 }
 
 }  // namespace
@@ -751,10 +870,13 @@ bool grouped_fits(const GroupedDesc& g) {
 
 // Token tile of a launch: the smallest width that holds twice the average
 // group, so that most groups are one tile; wider tiles read each weight fewer
-// times, narrower ones keep more stages of weights in flight.
-static int token_tile(int64_t tokens, int experts) {
+// times, narrower ones keep more stages of weights in flight. Halved while
+// that leaves CTA pairs without a tile.
+static int token_tile(int64_t tokens, int experts, int64_t mt) {
   const int64_t want = 2 * ((tokens + experts - 1) / experts);
-  return want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+  int nt = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+  while (nt > 32 && mt * ((tokens + nt - 1) / nt) * 2 <= num_sms() / 2) nt /= 2;
+  return nt;
 }
 
 muon_status grouped_rows(const GroupedDesc& g, const void* x, const void* w, void* y, bool mn, uint64_t timeout_ns,
@@ -766,7 +888,7 @@ muon_status grouped_rows(const GroupedDesc& g, const void* x, const void* w, voi
   p.K = (int)(mn ? g.n : g.k);
   const int64_t ldi = mn ? g.ldy : g.ldx;
   p.ldo = mn ? g.ldx : g.ldy;
-  const int nt = token_tile(g.tokens, g.experts);
+  const int nt = token_tile(g.tokens, g.experts, (p.M + grp::TILE_M - 1) / grp::TILE_M);
   if (!make_tensor_map(&p.mapA, g.type, w, g.k, g.n, g.experts, g.ldw, g.w_stride, mn ? 64 : grp::BM)) return MUON_ERR_CUDA;
   if (!make_tensor_map(&p.mapB, g.type, x, p.K, g.tokens, 1, ldi, 0, nt / 2)) return MUON_ERR_CUDA;
   p.offsets = g.offsets;
@@ -779,7 +901,11 @@ muon_status grouped_rows(const GroupedDesc& g, const void* x, const void* w, voi
   return g.type == Op::BF16 ? rows_typed<__nv_bfloat16>(p, nt, s) : rows_typed<__half>(p, nt, s);
 }
 
-size_t grouped_ws(int experts) { return (size_t)experts * 2 * sizeof(CUtensorMap) + 128; }
+// The maps of every expert, and one part's sum per CTA pair.
+static size_t maps_bytes(int experts) { return ((size_t)experts * 2 * sizeof(CUtensorMap) + 1023) / 1024 * 1024; }
+size_t grouped_ws(int experts) {
+  return 1024 + maps_bytes(experts) + (size_t)(num_sms() / 2) * grp::TILE_M * 256 * sizeof(float);
+}
 
 muon_status grouped_dw(const GroupedDesc& g, const void* dy, const void* x, void* dw, Op out, float alpha, float beta,
                        void* ws, uint64_t timeout_ns, cudaStream_t s) {
@@ -791,14 +917,15 @@ muon_status grouped_dw(const GroupedDesc& g, const void* dy, const void* x, void
     if (!make_tensor_map(&p.mapA, g.type, dy, g.n, g.tokens, 1, g.ldy, 0, 64)) return MUON_ERR_CUDA;
     if (!make_tensor_map(&p.mapB, g.type, x, g.k, g.tokens, 1, g.ldx, 0, 64)) return MUON_ERR_CUDA;
   }
-  p.clipped = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(ws) + 127) & ~uintptr_t(127));
+  const uintptr_t base = (reinterpret_cast<uintptr_t>(ws) + 1023) & ~uintptr_t(1023);
+  p.clipped = reinterpret_cast<CUtensorMap*>(base);
+  p.partial = reinterpret_cast<float*>(base + maps_bytes(g.experts));
   p.offsets = g.offsets;
   p.out = dw;
   p.ldo = g.ldw;
   p.so = g.w_stride;
   p.tokens = (int)g.tokens;
   p.experts = g.experts;
-  p.vec = 1;
   p.alpha = alpha;
   p.beta = beta;
   p.status = g.status;
