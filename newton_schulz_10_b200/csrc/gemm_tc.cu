@@ -1143,6 +1143,20 @@ bool make_tensor_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int6
   return make_map(m, t, base, inner, outer, batch, ld, bstride, box_outer);
 }
 
+bool make_block_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
+                    int64_t bstride) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const CUtensorMapDataType dt = t == Op::BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t es = op_size(t);
+  cuuint64_t dims[4] = {64, (cuuint64_t)outer, (cuuint64_t)(inner / 64), (cuuint64_t)batch};
+  cuuint64_t strides[3] = {(cuuint64_t)ld * es, 64 * es, (cuuint64_t)(batch > 1 ? bstride : ld * outer) * es};
+  cuuint32_t box[4] = {64, 64, 2, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, dt, batch > 0 ? 4 : 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 void set_gemm_pair_mode(int pair) { g_pair_mode = pair == 1 ? 1 : 2; }
 
 namespace {

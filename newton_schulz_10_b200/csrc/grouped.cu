@@ -32,6 +32,12 @@
 // parts, one work unit each, whose fp32 sums go to the workspace (at most one
 // per CTA pair); a second launch adds them in order.
 //
+// Issuing a tensor copy takes a thread about 235 ns whatever its size, a
+// k-block's products 270: so an operand is one copy per k-block (an MN-major
+// one, 64 columns wide by its swizzle, through a map that has the 64-column
+// blocks as a dimension of their own), and two threads take turns with the M
+// side, which alone decides how fast a launch of a few tiles streams weights.
+//
 // Every wait is bounded as in the Newton-Schulz GEMM; offsets are clamped to
 // 0..tokens before use, and a decreasing or out-of-range entry is reported as
 // MUON_ERR_INVALID_ARG.
@@ -60,10 +66,10 @@ constexpr uint64_t DRAIN_NS = 1000000000ull;
 // The tensor core truncates each addition to an fp32 accumulator, which
 // shrinks a long sum a little with every instruction (measured: an fp32 dW of
 // 1024 rows is 9.7e-7 off, in proportion to the rows). Sums into fp32 outputs
-// are therefore cut every 512 rows (8 k-blocks) and the parts added with
+// are therefore cut every 768 rows (12 k-blocks) and the parts added with
 // rounding to nearest, in order, by the same threads; a part's epilogue
 // overlaps the next part's products.
-constexpr int kPartBlocks = 8;
+constexpr int kPartBlocks = 12;
 
 enum : int { ROWS = 0, DW = 1 };
 
@@ -72,7 +78,8 @@ struct Cfg {
   static constexpr int A_STAGE = BM * BK * 2;
   static constexpr int B_STAGE = (NT / 2) * BK * 2;
   static constexpr int TX_BYTES = 2 * (A_STAGE + B_STAGE);  // per stage, both CTAs
-  static constexpr int STAGES = NT == 256 ? 6 : NT == 128 ? 8 : NT == 64 ? 9 : 10;
+  static constexpr int STAGES = NT == 256 ? 6 : NT <= 64 ? 10 : 8;
+  static_assert(STAGES % 2 == 0, "each of the two M-side producers keeps its stages");
   static constexpr int EPI_BUF = MODE == ROWS ? 2048 : 4096;  // one 32x32 block per warp (16-bit, fp32)
   static constexpr int TABLE = MODE == ROWS ? (kMaxExperts + 1 + 32) * 4 : 0;
   static constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * EPI_BUF + TABLE + (2 * STAGES + 5) * 8 + 64;
@@ -89,6 +96,7 @@ struct Params {
   int tokens, experts;
   int M, N, K;            // ROWS: M = features out, K = features in; DW: M = n, N = k
   int a_mn;               // ROWS: W read MN-major
+  int a_one, b_one;       // an MN-major operand's boxes are one copy (its width is a multiple of 64)
   int splits;             // DW: parts of an expert's rows (1: none, results go to out)
   float* partial;         // DW, splits > 1: 256 x 256 fp32 per (tile, part)
   float alpha, beta;      // DW
@@ -197,29 +205,47 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* 
 }
 
 // Early exit of a pair: wait until every operand copy that either CTA issued
-// has landed. cnt: k-blocks issued by the leader's A and B producers and the
-// follower's. Blocks before max(cnt) - STAGES have been consumed; each later
-// one occupies its own stage, whose barrier is settled for the copies that
-// were never issued and then waited on.
+// has landed. cnt: k-blocks issued by each CTA's producers (M side of even
+// and of odd k-blocks, N side; the leader's, then the follower's). Blocks
+// STAGES before the last one issued have been consumed; each later one
+// occupies its own stage, whose barrier is settled for the copies that were
+// never issued and then waited on.
 template <int MODE, int NT>
 __device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
   using Cf = Cfg<MODE, NT>;
-  const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
-  const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
+  // whether producer x (0, 1: M side, 2: N side; + 3: the follower's) issued block j
+  auto has = [&](int x, int j) {
+    const int kind = x % 3;
+    return kind == 2 ? j < cnt[x] : (j & 1) == kind && (j >> 1) < cnt[x];
+  };
   int hi = 0;
-  for (int x = 0; x < 4; ++x) hi = c[x] > hi ? c[x] : hi;
+  for (int x = 0; x < 6; ++x) {
+    const int kind = x % 3, last = kind == 2 ? cnt[x] : cnt[x] > 0 ? 2 * (cnt[x] - 1) + kind + 1 : 0;
+    hi = last > hi ? last : hi;
+  }
   for (int j = hi > Cf::STAGES ? hi - Cf::STAGES : 0; j < hi; ++j) {
     uint32_t issued = 0;
-    for (int x = 0; x < 4; ++x)
-      if (j < c[x]) issued += bytes[x];
+    for (int x = 0; x < 6; ++x)
+      if (has(x, j)) issued += x % 3 == 2 ? Cf::B_STAGE : Cf::A_STAGE;
     uint64_t* bar = &full[j % Cf::STAGES];
-    if (j < c[0]) {
+    if (has(j & 1, j)) {
       if (issued < (uint32_t)Cf::TX_BYTES) mbar_complete_tx(bar, Cf::TX_BYTES - issued);
     } else {
       mbar_arrive_expect_tx(bar, issued);
     }
     drain_wait(bar, (uint32_t)((j / Cf::STAGES) & 1), status);
   }
+}
+
+// tma_load_3d_pair with a fourth coordinate
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                                 uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(c0),
+      "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
 
 __device__ __forceinline__ void fence_map_acquire(const CUtensorMap* m) {
@@ -320,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) issued_cnt[i] = 0;
+    for (int i = 0; i < 6; ++i) issued_cnt[i] = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -331,6 +357,11 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     prefetch_tmap(&p.mapA);
     prefetch_tmap(&p.mapB);
   }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // barriers initialised in both CTAs
+  tc_fence_after();
+  // all of the above overlaps the previous launch's end
   grid_dependency_wait();
   grid_dependents_launch();
   const int mt = (p.M + TILE_M - 1) / TILE_M;
@@ -373,21 +404,20 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       if (e0 + i < p.experts) table[e0 + i] = base;
       base += c[i];
     }
+    __syncthreads();
     total = all * mt;
   } else {
     total = p.experts * mt * ntl * p.splits;
   }
-  tc_fence_before();
-  __syncwarp();
-  cluster_sync();  // barriers initialised in both CTAs, table written
-  tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t budget = p.timeout_ns;
 
-  if ((warp == 0 || warp == 3) && lane == 0) {
-    // TMA producers: warp 0 the M side (and the leader's byte count), warp 3
-    // the N side; both take part in every phase of every stage.
-    const bool issues_a = warp == 0;
+  if (warp != 1 && warp < EPI_WARP0 && lane == 0) {
+    // TMA producers: warps 0 and 2 the M side of even and odd k-blocks (and
+    // the leader's byte count), warp 3 the N side. STAGES is even, so each
+    // takes part in every phase of its stages.
+    const bool issues_a = warp != 3;
+    const int turn = warp >> 1;  // 0 or 1: the k-blocks (counted over all tiles) of an M-side producer
     int stage = 0;
     uint32_t phase = 0;
     int issued = 0;
@@ -406,39 +436,46 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         }
       }
       for (int kb = 0; kb < t.nkb; ++kb) {
-        if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status)) {
-          raise_peer();
-          ok = false;
-          break;
-        }
-        if (issues_a && rank == 0) mbar_arrive_expect_tx(&full[stage], Cf::TX_BYTES);
-        uint8_t* a = sA + stage * Cf::A_STAGE;
-        uint8_t* b = sB + stage * Cf::B_STAGE;
-        const int k0 = kb * BK;
-        if (MODE == ROWS) {
-          if (!issues_a) {
-            tma_load_3d_pair(b, map, k0, bn0, 0, &full[stage]);
-          } else if (!p.a_mn) {
-            tma_load_3d_pair(a, map, k0, am0, t.e, &full[stage]);
-          } else {
-            tma_load_3d_pair(a, map, am0, k0, t.e, &full[stage]);
-            tma_load_3d_pair(a + 8192, map, am0 + 64, k0, t.e, &full[stage]);
+        if (!issues_a || (stage & 1) == turn) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status)) {
+            raise_peer();
+            ok = false;
+            break;
           }
-        } else {
-          uint8_t* d = issues_a ? a : b;
-          const int c0 = issues_a ? am0 : bn0;
-          constexpr int NB = NT / 2 / 64;
-          tma_load_3d_pair(d, map, c0, t.t0 + k0, 0, &full[stage]);
-          if (issues_a || NB > 1) tma_load_3d_pair(d + 8192, map, c0 + 64, t.t0 + k0, 0, &full[stage]);
+          if (issues_a && rank == 0) mbar_arrive_expect_tx(&full[stage], Cf::TX_BYTES);
+          uint8_t* a = sA + stage * Cf::A_STAGE;
+          uint8_t* b = sB + stage * Cf::B_STAGE;
+          const int k0 = kb * BK;
+          if (MODE == ROWS) {
+            if (!issues_a) {
+              tma_load_3d_pair(b, map, k0, bn0, 0, &full[stage]);
+            } else if (!p.a_mn) {
+              tma_load_3d_pair(a, map, k0, am0, t.e, &full[stage]);
+            } else if (p.a_one) {
+              tma_load_4d_pair(a, map, 0, k0, am0 >> 6, t.e, &full[stage]);
+            } else {
+              tma_load_3d_pair(a, map, am0, k0, t.e, &full[stage]);
+              tma_load_3d_pair(a + 8192, map, am0 + 64, k0, t.e, &full[stage]);
+            }
+          } else {
+            uint8_t* d = issues_a ? a : b;
+            const int c0 = issues_a ? am0 : bn0;
+            if (issues_a ? p.a_one : p.b_one) {
+              tma_load_3d_pair(d, map, 0, t.t0 + k0, c0 >> 6, &full[stage]);
+            } else {
+              tma_load_3d_pair(d, map, c0, t.t0 + k0, 0, &full[stage]);
+              tma_load_3d_pair(d + 8192, map, c0 + 64, t.t0 + k0, 0, &full[stage]);
+            }
+          }
+          ++issued;
         }
-        ++issued;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-    const uint32_t slot = smem_u32(const_cast<int*>(issued_cnt + 2 * rank + (issues_a ? 0 : 1)));
+    const uint32_t slot = smem_u32(const_cast<int*>(issued_cnt + 3 * rank + (issues_a ? turn : 2)));
     st_cluster_u32(mapa_shared(slot, 0), (uint32_t)issued);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // MMA issuer (the leader issues for the pair)
@@ -513,6 +550,29 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       const int parts = parts_of<MODE, O>(t.nkb);
       for (int part = 0; part < parts; ++part) {
       const float beta = part == 0 ? p.beta : 1.f;
+      const int r0 = t.m0 + (int)rank * BM + q * 32;  // first M-side row of this warp
+      float4 ahead[8];
+      // DW, beta: row 4 j + lane / 8, columns c + 4 (lane % 8).. of the block at column c
+      auto load_old = [&](int c) {
+        const O* d = reinterpret_cast<const O*>(t.whole ? p.out : p.partial) +
+                     (t.whole ? (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0 : (long long)tile * (TILE_M * NT));
+        const long long ldo = t.whole ? p.ldo : NT;
+        const int cols = p.N - t.n0 - c, rows = p.M - r0, cc = (lane & 7) * 4;
+        d += (r0 - t.m0 + (lane >> 3)) * ldo + c + cc;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (4 * j + (lane >> 3) >= rows || cc >= cols) continue;
+          if (cc + 4 <= cols) {
+            ahead[j] = load_out4<O>(d + 4 * j * ldo);
+          } else {
+            float* o = &ahead[j].x;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (cc + x < cols) o[x] = out_to_f<O>(d[4 * j * ldo + x]);
+          }
+        }
+      };
+      if (MODE == DW && beta != 0.f && (t.whole || t.nkb > 0)) load_old(half * 32);
       const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, budget, p.status);
       go = __all_sync(0xffffffffu, ok);
       if (!go) {
@@ -520,7 +580,6 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         break;
       }
       tc_fence_after();
-      const int r0 = t.m0 + (int)rank * BM + q * 32;  // first M-side row of this warp
       const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + acc * ACC_COLS;
       if (MODE == ROWS) {
         // block: lanes = features r0.., columns = tokens; stored transposed
@@ -623,23 +682,12 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
           }
           const int cc = (lane & 7) * 4;
           O* const at = out + (wr + (lane >> 3)) * ldo + c + cc;  // row 4 j + lane / 8 at at + 4 j ldo
+          // what is added to: this chunk's was loaded while the one before was
+          // worked on (the first chunk's before the accumulator was waited for)
           float4 old[8];
-          if (beta != 0.f) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              old[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (4 * j + (lane >> 3) >= rows || cc >= cols) continue;
-              const O* d = at + 4 * j * ldo;
-              if (cc + 4 <= cols) {
-                old[j] = load_out4<O>(d);
-              } else {
-                float* o = &old[j].x;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  if (cc + x < cols) o[x] = out_to_f<O>(d[x]);
-              }
-            }
-          }
+          for (int j = 0; j < 8; ++j) old[j] = ahead[j];
+          if (beta != 0.f && c + 64 < NT) load_old(c + 64);
           uint32_t raw[32];
           if (t.nkb > 0) {
             tmem_ld_32x32(trow + c, raw);
@@ -889,7 +937,10 @@ muon_status grouped_rows(const GroupedDesc& g, const void* x, const void* w, voi
   const int64_t ldi = mn ? g.ldy : g.ldx;
   p.ldo = mn ? g.ldx : g.ldy;
   const int nt = token_tile(g.tokens, g.experts, (p.M + grp::TILE_M - 1) / grp::TILE_M);
-  if (!make_tensor_map(&p.mapA, g.type, w, g.k, g.n, g.experts, g.ldw, g.w_stride, mn ? 64 : grp::BM)) return MUON_ERR_CUDA;
+  p.a_one = mn && g.k % 64 == 0;
+  const bool made = p.a_one ? make_block_map(&p.mapA, g.type, w, g.k, g.n, g.experts, g.ldw, g.w_stride)
+                            : make_tensor_map(&p.mapA, g.type, w, g.k, g.n, g.experts, g.ldw, g.w_stride, mn ? 64 : grp::BM);
+  if (!made) return MUON_ERR_CUDA;
   if (!make_tensor_map(&p.mapB, g.type, x, p.K, g.tokens, 1, ldi, 0, nt / 2)) return MUON_ERR_CUDA;
   p.offsets = g.offsets;
   p.out = y;
@@ -914,8 +965,13 @@ muon_status grouped_dw(const GroupedDesc& g, const void* dy, const void* x, void
   p.M = (int)g.n;
   p.N = (int)g.k;
   if (g.tokens > 0) {  // without rows no copy reads the maps
-    if (!make_tensor_map(&p.mapA, g.type, dy, g.n, g.tokens, 1, g.ldy, 0, 64)) return MUON_ERR_CUDA;
-    if (!make_tensor_map(&p.mapB, g.type, x, g.k, g.tokens, 1, g.ldx, 0, 64)) return MUON_ERR_CUDA;
+    p.a_one = g.n % 64 == 0;
+    p.b_one = g.k % 64 == 0;
+    if (!(p.a_one ? make_block_map(&p.mapA, g.type, dy, g.n, g.tokens, 0, g.ldy, 0)
+                  : make_tensor_map(&p.mapA, g.type, dy, g.n, g.tokens, 1, g.ldy, 0, 64)) ||
+        !(p.b_one ? make_block_map(&p.mapB, g.type, x, g.k, g.tokens, 0, g.ldx, 0)
+                  : make_tensor_map(&p.mapB, g.type, x, g.k, g.tokens, 1, g.ldx, 0, 64)))
+      return MUON_ERR_CUDA;
   }
   const uintptr_t base = (reinterpret_cast<uintptr_t>(ws) + 1023) & ~uintptr_t(1023);
   p.clipped = reinterpret_cast<CUtensorMap*>(base);

@@ -90,6 +90,13 @@ int num_sms();
 bool make_tensor_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
                      int64_t bstride, int box_outer);
 
+// The same memory for MN-major operands whose width `inner` is a multiple of
+// 64: [batch][inner / 64][outer][64], box {64, 64, 2, 1}, so that one copy
+// brings two 64-column blocks of 64 rows (8 KB each, one after the other).
+// batch = 0: no batch dimension (three coordinates).
+bool make_block_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
+                    int64_t bstride);
+
 // Products grouped by expert (grouped.cu). Checked arguments of one call:
 // x is tokens x k (ldx), y / dy tokens x n (ldy), W_e n x k (ldw, w_stride).
 struct GroupedDesc {
