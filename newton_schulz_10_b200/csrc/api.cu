@@ -1045,8 +1045,8 @@ muon_status check_stacks(const muon_stack* st, int32_t count, const muon_stack_p
 
 // Small matrices are updated by one launch with the matrix on chip, which
 // needs no workspace; the rest by row kernels and the chain of products.
-bool resident(const muon_stack& k, const muon_ns_params* ns, Op t) {
-  return t != Op::F32 && !ns->gram && resident_fits(k.rows, k.cols);
+bool resident(const muon_stack& k, const muon_ns_params* ns, Op t, int planes) {
+  return t != Op::F32 && !ns->gram && resident_fits(k.rows, k.cols, k.count, ns->T, planes, nullptr);
 }
 
 struct StackPlan {
@@ -1065,7 +1065,7 @@ StackPlan plan_stacks(const muon_stack* st, int32_t count, const muon_ns_params*
   size_t rows = 0, mats = 0;
   for (int i = 0; i < count; ++i) {
     if (empty_stack(st[i])) continue;
-    if (resident(st[i], ns, t)) {
+    if (resident(st[i], ns, t, planes)) {
       q.small.push_back(i);
       continue;
     }

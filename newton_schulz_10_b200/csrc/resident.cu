@@ -616,24 +616,32 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
 
 namespace {
 
+// The kernel's attributes, once per device.
 template <typename T, int PL>
-muon_status launch_resident(const res::Params& p, cudaStream_t s) {
+muon_status set_up() {
   static std::mutex mu;
   static bool ready[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!ready[dev]) {
-      if (cudaFuncSetAttribute(res::stack_resident<T, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               res::SMEM_MAX) != cudaSuccess ||
-          cudaFuncSetAttribute(res::stack_resident<T, PL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-        cudaGetLastError();
-        return MUON_ERR_CUDA;
-      }
-      ready[dev] = true;
-    }
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return MUON_ERR_CUDA;
   }
+  std::lock_guard<std::mutex> lock(mu);
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(res::stack_resident<T, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, res::SMEM_MAX) != cudaSuccess ||
+        cudaFuncSetAttribute(res::stack_resident<T, PL>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+      cudaGetLastError();
+      return MUON_ERR_CUDA;
+    }
+    ready[dev] = true;
+  }
+  return MUON_OK;
+}
+
+template <typename T, int PL>
+muon_status launch_resident(const res::Params& p, cudaStream_t s) {
+  const muon_status up = set_up<T, PL>();
+  if (up != MUON_OK) return up;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.m.count * p.C));
   cfg.blockDim = dim3(res::THREADS);
@@ -654,8 +662,82 @@ muon_status launch_resident(const res::Params& p, cudaStream_t s) {
 
 }  // namespace
 
-bool resident_fits(int64_t rows, int64_t cols) {
-  return std::min(rows, cols) <= res::MAX_N && std::max(rows, cols) <= res::MAX_M;
+namespace {
+
+// Clusters of C CTAs (one per SM) that can run at once on the current device.
+int cluster_capacity(int C) {
+  static std::mutex mu;
+  static int cap[64][5];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return num_sms() / C;
+  }
+  int k = 0;
+  while ((1 << k) < C) ++k;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = cap[dev][k];
+  if (n == 0) {
+    n = num_sms() / C;
+    if (C > 1 && set_up<__half, 2>() == MUON_OK) {
+      cudaLaunchConfig_t q = {};
+      q.gridDim = dim3((unsigned)(n * C));
+      q.blockDim = dim3(res::THREADS);
+      q.dynamicSmemBytes = res::SMEM_MAX;
+      cudaLaunchAttribute a[1];
+      a[0].id = cudaLaunchAttributeClusterDimension;
+      a[0].val.clusterDim.x = (unsigned)C;
+      a[0].val.clusterDim.y = 1;
+      a[0].val.clusterDim.z = 1;
+      q.attrs = a;
+      q.numAttrs = 1;
+      int c = 0;
+      if (cudaOccupancyMaxActiveClusters(&c, res::stack_resident<__half, 2>, &q) == cudaSuccess && c > 0 && c < n) n = c;
+      cudaGetLastError();
+    }
+    if (n < 1) n = 1;
+  }
+  return n;
+}
+
+}  // namespace
+
+// The cluster size, by a model of the step in cycles (measured with the clock
+// register at np = 64 and 128, g = 1 to 4, C = 1 to 8): an instruction of the
+// products takes at least 75 cycles, an epilogue 700 a group of X and 75 per
+// four rows and columns of B', the exchange 1700 + 0.55 np^2 whatever C is,
+// loads and stores 0.4 an element. Larger clusters halve the work on X and
+// pay the exchange: 12 x 64 x 768 takes 46 us on 8 CTAs a matrix and 52 on 4,
+// 1 x 128 x 128 takes 69 on 2 and 49 on 1, 16 x 128 x 512 (two waves of
+// clusters of 8) 146 on 8 and 76 on 2.
+//
+// A stack of many matrices that need large clusters is left to the chain of
+// launches, whose time is about 20 us a step for its latencies and its padded
+// products at 0.8 PFLOP/s: 48 x 128 x 2048 takes 631 us here and 505 there,
+// 48 x 64 x 2048 221 here and 407 there.
+bool resident_fits(int64_t rows, int64_t cols, int64_t count, int T, int planes, int* C_out) {
+  const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
+  if (n > res::MAX_N || m > res::MAX_M) return false;
+  const int groups = (int)((m + 63) / 64), np = (int)((n + 15) / 16 * 16);
+  double best = 0.0;
+  int best_C = 0;
+  for (int C = 1; C <= res::MAX_C; C *= 2) {
+    const int g = (groups + C - 1) / C;
+    if (g > res::MAX_G || res::smem_bytes(g, np, C) > res::SMEM_MAX) continue;
+    if (C > 8 && best_C) break;  // only where a smaller cluster cannot hold the matrix
+    const double step = 2000.0 + 900.0 * g + 14.0 * np + std::max(14.0 * np, 6.6 * np * g) + 700.0 * g + 19.0 * np +
+                        (C > 1 ? 1700.0 + 0.55 * np * np : 1000.0);
+    const double waves = (double)((count + cluster_capacity(C) - 1) / cluster_capacity(C));
+    const double t = waves * (12000.0 + 0.4 * n * 64 * g + T * step);
+    if (!best_C || t < best) {
+      best = t;
+      best_C = C;
+    }
+  }
+  const double N = 256.0, tile = (double)(m + 127) / 128 * 128;
+  const double chain = 20.0 * T + 2.0 * count * T * (N * N * tile + N * N * np + N * tile * np) * (planes == 2 ? 3.0 : 1.0) / 0.8e9;
+  if (C_out) *C_out = best_C;
+  return best_C > 0 && 1.25 * best / 1850.0 <= chain;  // the model is 10 to 20% low
 }
 
 muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns, Op t, int planes, float kappa, float rho,
@@ -666,15 +748,9 @@ muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns
   p.n = p.tall ? p.m.cols : p.m.rows;
   p.long_side = p.tall ? p.m.rows : p.m.cols;
   p.np = (p.n + 15) / 16 * 16;
-  // The smallest cluster that holds the matrix; a larger one while the GPU
-  // has SMs to spare, since half the columns a CTA halve two of the three
-  // products.
-  const int groups = (p.long_side + 63) / 64;
-  auto per_cta = [&](int C) { return (groups + C - 1) / C; };
-  p.C = 1;
-  while (per_cta(p.C) > res::MAX_G || res::smem_bytes(per_cta(p.C), p.np, p.C) > res::SMEM_MAX) p.C *= 2;
-  while (p.C < 8 && per_cta(p.C) > 1 && (int64_t)p.m.count * p.C * 2 <= num_sms()) p.C *= 2;
-  p.g = per_cta(p.C);
+  resident_fits(p.m.rows, p.m.cols, p.m.count, ns.T, planes, &p.C);
+  if (p.C < 1) return MUON_ERR_INVALID_ARG;
+  p.g = ((p.long_side + 63) / 64 + p.C - 1) / p.C;
   p.mu = L.mu;
   p.step = L.step;
   p.keep = L.keep;

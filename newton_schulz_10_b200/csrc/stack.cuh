@@ -51,9 +51,10 @@ muon_status launch_stack_cast(const StackLaunch& L, Op t, int planes, cudaStream
 muon_status launch_stack_update(const StackLaunch& L, Op t, int planes, cudaStream_t s);
 
 // The whole update of one stack (L.m[0]) of small matrices in one launch
-// (resident.cu): whether the shape allows it, and the launch. kappa and rho
-// are the storage scales of X and of the n x n matrices.
-bool resident_fits(int64_t rows, int64_t cols);
+// (resident.cu): whether that is the faster way for T steps on this device
+// (and the CTAs per matrix), and the launch. kappa and rho are the storage
+// scales of X and of the n x n matrices.
+bool resident_fits(int64_t rows, int64_t cols, int64_t count, int T, int planes, int* C_out);
 muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns, Op t, int planes, float kappa, float rho,
                                   uint64_t timeout_ns, cudaStream_t s);
 
