@@ -32,10 +32,10 @@
 // parts, one work unit each, whose fp32 sums go to the workspace (at most one
 // per CTA pair); a second launch adds them in order.
 //
-// Issuing a tensor copy takes a thread about 235 ns whatever its size, a
-// k-block's products 270: so an operand is one copy per k-block (an MN-major
+// The issuing roles are whole warps (common.cuh: 491 -> 444 us for 32768 rows
+// of 2048 into 64 x 4096). An operand is one copy per k-block (an MN-major
 // one, 64 columns wide by its swizzle, through a map that has the 64-column
-// blocks as a dimension of their own), and two threads take turns with the M
+// blocks as a dimension of their own), and two warps take turns with the M
 // side, which alone decides how fast a launch of a few tiles streams weights.
 //
 // Every wait is bounded as in the Newton-Schulz GEMM; offsets are clamped to
@@ -237,17 +237,6 @@ __device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int*
   }
 }
 
-// tma_load_3d_pair with a fourth coordinate
-__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                                 uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(c0),
-      "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 __device__ __forceinline__ void fence_map_acquire(const CUtensorMap* m) {
   asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
@@ -412,7 +401,8 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t budget = p.timeout_ns;
 
-  if (warp != 1 && warp < EPI_WARP0 && lane == 0) {
+  if (warp != 1 && warp < EPI_WARP0) {
+    const uint32_t on = elect_one();
     // TMA producers: warps 0 and 2 the M side of even and odd k-blocks (and
     // the leader's byte count), warp 3 the N side. STAGES is even, so each
     // takes part in every phase of its stages.
@@ -438,33 +428,34 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       for (int kb = 0; kb < t.nkb; ++kb) {
         if (!issues_a || (stage & 1) == turn) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status)) {
-            raise_peer();
+            if (on) raise_peer();
             ok = false;
-            break;
           }
-          if (issues_a && rank == 0) mbar_arrive_expect_tx(&full[stage], Cf::TX_BYTES);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (issues_a && rank == 0) mbar_arrive_expect_tx_if(on, &full[stage], Cf::TX_BYTES);
           uint8_t* a = sA + stage * Cf::A_STAGE;
           uint8_t* b = sB + stage * Cf::B_STAGE;
           const int k0 = kb * BK;
           if (MODE == ROWS) {
             if (!issues_a) {
-              tma_load_3d_pair(b, map, k0, bn0, 0, &full[stage]);
+              tma_load_3d_pair_if(on, b, map, k0, bn0, 0, &full[stage]);
             } else if (!p.a_mn) {
-              tma_load_3d_pair(a, map, k0, am0, t.e, &full[stage]);
+              tma_load_3d_pair_if(on, a, map, k0, am0, t.e, &full[stage]);
             } else if (p.a_one) {
-              tma_load_4d_pair(a, map, 0, k0, am0 >> 6, t.e, &full[stage]);
+              tma_load_4d_pair_if(on, a, map, 0, k0, am0 >> 6, t.e, &full[stage]);
             } else {
-              tma_load_3d_pair(a, map, am0, k0, t.e, &full[stage]);
-              tma_load_3d_pair(a + 8192, map, am0 + 64, k0, t.e, &full[stage]);
+              tma_load_3d_pair_if(on, a, map, am0, k0, t.e, &full[stage]);
+              tma_load_3d_pair_if(on, a + 8192, map, am0 + 64, k0, t.e, &full[stage]);
             }
           } else {
             uint8_t* d = issues_a ? a : b;
             const int c0 = issues_a ? am0 : bn0;
             if (issues_a ? p.a_one : p.b_one) {
-              tma_load_3d_pair(d, map, 0, t.t0 + k0, c0 >> 6, &full[stage]);
+              tma_load_3d_pair_if(on, d, map, 0, t.t0 + k0, c0 >> 6, &full[stage]);
             } else {
-              tma_load_3d_pair(d, map, c0, t.t0 + k0, 0, &full[stage]);
-              tma_load_3d_pair(d + 8192, map, c0 + 64, t.t0 + k0, 0, &full[stage]);
+              tma_load_3d_pair_if(on, d, map, c0, t.t0 + k0, 0, &full[stage]);
+              tma_load_3d_pair_if(on, d + 8192, map, c0 + 64, t.t0 + k0, 0, &full[stage]);
             }
           }
           ++issued;
@@ -476,9 +467,10 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       }
     }
     const uint32_t slot = smem_u32(const_cast<int*>(issued_cnt + 3 * rank + (issues_a ? turn : 2)));
-    st_cluster_u32(mapa_shared(slot, 0), (uint32_t)issued);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+    if (on) st_cluster_u32(mapa_shared(slot, 0), (uint32_t)issued);
+  } else if (warp == 1 && rank == 0) {
     // MMA issuer (the leader issues for the pair)
+    const uint32_t on = elect_one();
     int stage = 0;
     uint32_t phase = 0;
     int acc = 0;
@@ -499,42 +491,42 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       const uint32_t idesc = idesc_f16(fmt, a_mn, b_mn, TILE_M, t.n_mma);
       const int parts = parts_of<MODE, O>(t.nkb);
       for (int part = 0; part < parts && ok; ++part) {
-      if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, budget, p.status)) {
-        raise_peer();
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
-      const int kb0 = part * kPartBlocks, kb1 = part + 1 < parts ? kb0 + kPartBlocks : t.nkb;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, budget, p.status)) {
-          raise_peer();
-          ok = false;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, budget, p.status));
+        if (!ok) {
+          if (on) raise_peer();
           break;
         }
-        const uint32_t a_lo = (a_base + stage * Cf::A_STAGE) >> 4, b_lo = (b_base + stage * Cf::B_STAGE) >> 4;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * ACC_COLS;
+        const int kb0 = part * kPartBlocks, kb1 = part + 1 < parts ? kb0 + kPartBlocks : t.nkb;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, abort_flag, budget, p.status));
+          if (!ok) {
+            if (on) raise_peer();
+            break;
+          }
+          const uint32_t a_lo = (a_base + stage * Cf::A_STAGE) >> 4, b_lo = (b_base + stage * Cf::B_STAGE) >> 4;
 #pragma unroll
-        for (int k = 0; k < BK / UMMA_K; ++k)
-          umma_f16_pair(d_tmem, a_hi | (uint64_t)(a_lo + k * (a_kstep >> 4)), b_hi | (uint64_t)(b_lo + k * (b_kstep >> 4)),
-                        idesc, kb != kb0 || k != 0);
-        umma_commit_pair(&empty[stage], 0x3);
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
+          for (int k = 0; k < BK / UMMA_K; ++k)
+            umma_f16_pair_if(on, d_tmem, a_hi | (uint64_t)(a_lo + k * (a_kstep >> 4)),
+                          b_hi | (uint64_t)(b_lo + k * (b_kstep >> 4)), idesc, kb != kb0 || k != 0);
+          umma_commit_pair_if(on, &empty[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_if(on, &tfull[acc], 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
         }
       }
-      if (!ok) break;
-      umma_commit_pair(&tfull[acc], 0x3);
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
-      }
-      }
     }
-    umma_commit_pair(drain, 0x3);
+    umma_commit_pair_if(on, drain, 0x3);
     drain_wait(drain, 0, p.status);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     drain_wait(drain, 0, p.status);  // the follower: no MMA reads its shared memory or writes its TMEM any more
   } else if (warp >= EPI_WARP0) {
     const int e = warp - EPI_WARP0;
@@ -549,191 +541,191 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
       const int parts = parts_of<MODE, O>(t.nkb);
       for (int part = 0; part < parts; ++part) {
-      const float beta = part == 0 ? p.beta : 1.f;
-      const int r0 = t.m0 + (int)rank * BM + q * 32;  // first M-side row of this warp
-      float4 ahead[8];
-      // DW, beta: row 4 j + lane / 8, columns c + 4 (lane % 8).. of the block at column c
-      auto load_old = [&](int c) {
-        const O* d = reinterpret_cast<const O*>(t.whole ? p.out : p.partial) +
-                     (t.whole ? (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0 : (long long)tile * (TILE_M * NT));
-        const long long ldo = t.whole ? p.ldo : NT;
-        const int cols = p.N - t.n0 - c, rows = p.M - r0, cc = (lane & 7) * 4;
-        d += (r0 - t.m0 + (lane >> 3)) * ldo + c + cc;
+        const float beta = part == 0 ? p.beta : 1.f;
+        const int r0 = t.m0 + (int)rank * BM + q * 32;  // first M-side row of this warp
+        float4 ahead[8];
+        // DW, beta: row 4 j + lane / 8, columns c + 4 (lane % 8).. of the block at column c
+        auto load_old = [&](int c) {
+          const O* d = reinterpret_cast<const O*>(t.whole ? p.out : p.partial) +
+                       (t.whole ? (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0 : (long long)tile * (TILE_M * NT));
+          const long long ldo = t.whole ? p.ldo : NT;
+          const int cols = p.N - t.n0 - c, rows = p.M - r0, cc = (lane & 7) * 4;
+          d += (r0 - t.m0 + (lane >> 3)) * ldo + c + cc;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (4 * j + (lane >> 3) >= rows || cc >= cols) continue;
-          if (cc + 4 <= cols) {
-            ahead[j] = load_out4<O>(d + 4 * j * ldo);
-          } else {
-            float* o = &ahead[j].x;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (cc + x < cols) o[x] = out_to_f<O>(d[4 * j * ldo + x]);
-          }
-        }
-      };
-      if (MODE == DW && beta != 0.f && (t.whole || t.nkb > 0)) load_old(half * 32);
-      const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, budget, p.status);
-      go = __all_sync(0xffffffffu, ok);
-      if (!go) {
-        if (lane == 0) raise_peer();
-        break;
-      }
-      tc_fence_after();
-      const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + acc * ACC_COLS;
-      if (MODE == ROWS) {
-        // block: lanes = features r0.., columns = tokens; stored transposed
-        O* const out = reinterpret_cast<O*>(p.out);
-        for (int c = half * 32; c < t.nvalid; c += 64) {
-          if (r0 >= p.M) break;  // warp-uniform
-          uint32_t f0[16], f1[16];
-          tmem_ld_16x256_x4(trow + c, f0);
-          tmem_ld_16x256_x4(trow + c + (16u << 16), f1);
-          tmem_wait_ld();
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int x = 4 * i + 2 * k;
-              pk[4 * k + i] = Elem<T>::pack2(__uint_as_float(f0[x]), __uint_as_float(f0[x + 1]));
-              pk[8 + 4 * k + i] = Elem<T>::pack2(__uint_as_float(f1[x]), __uint_as_float(f1[x + 1]));
-            }
-          __syncwarp();  // the previous chunk has been read
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            stsm_x4_trans(sd_a + sw64(lane, 16 * (k >> 1) + 8 * (k & 1)), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2],
-                          pk[4 * k + 3]);
-          __syncwarp();
-          // rows of 32 features: four lanes a row, 16 bytes a lane
-          const int f = r0 + (lane & 3) * 8;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int tk = 8 * j + (lane >> 2);
-            if (c + tk >= t.nvalid || f >= p.M) continue;
-            const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(tk, (lane & 3) * 8));
-            O* d = out + (long long)(t.n0 + c + tk) * p.ldo + f;
-            if (f + 8 <= p.M) {
-              *reinterpret_cast<uint4*>(d) = v;
+          for (int j = 0; j < 8; ++j) {
+            if (4 * j + (lane >> 3) >= rows || cc >= cols) continue;
+            if (cc + 4 <= cols) {
+              ahead[j] = load_out4<O>(d + 4 * j * ldo);
             } else {
-              const O* h = reinterpret_cast<const O*>(&v);
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                if (f + x < p.M) d[x] = h[x];
-            }
-          }
-        }
-      } else {
-        // block: lanes = rows of dW_e, columns = its columns; staged so that
-        // neighbouring lanes hold neighbouring columns. A part of a tile goes
-        // to its 256 x 256 place in the workspace (none when it has no rows).
-        const bool skip = !t.whole && t.nkb == 0;
-        O* const out = t.whole ? reinterpret_cast<O*>(p.out) + (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0
-                               : reinterpret_cast<O*>(p.partial) + (long long)tile * (TILE_M * NT);
-        const long long ldo = t.whole ? p.ldo : NT;
-        const int rows = skip ? 0 : min(p.M - r0, 32), wr = r0 - t.m0;  // rows of this warp, from row wr of the tile
-        for (int c = half * 32; c < NT; c += 64) {
-          const int cols = p.N - t.n0 - c;
-          if (rows <= 0 || cols <= 0) break;  // warp-uniform
-          if (t.nkb == 0 && beta == 0.f) {
-            constexpr int V = 16 / sizeof(O);  // no rows, nothing to add to: zeros
-            for (int i = lane; i < rows * (32 / V); i += 32) {
-              const int r = i / (32 / V), x0 = (i % (32 / V)) * V;
-              O* d = out + (wr + r) * ldo + c + x0;
-              if (x0 + V <= cols) *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
-              else
-                for (int x = 0; x < V; ++x)
-                  if (x0 + x < cols) d[x] = f_to_out<O>(0.f);
-            }
-            continue;
-          }
-          if (!std::is_same<O, float>::value && beta == 0.f) {
-            // 16-bit result alone: rounded before it is staged, four lanes a row
-            uint32_t raw[32];
-            tmem_ld_32x32(trow + c, raw);
-            tmem_wait_ld();
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t h[4];
+              float* o = &ahead[j].x;
 #pragma unroll
               for (int x = 0; x < 4; ++x)
-                h[x] = Elem<T>::pack2(p.alpha * __uint_as_float(raw[8 * k + 2 * x]), p.alpha * __uint_as_float(raw[8 * k + 2 * x + 1]));
-              *reinterpret_cast<uint4*>(sd + sw64(lane, 8 * k)) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (cc + x < cols) o[x] = out_to_f<O>(d[4 * j * ldo + x]);
             }
+          }
+        };
+        if (MODE == DW && beta != 0.f && (t.whole || t.nkb > 0)) load_old(half * 32);
+        const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, budget, p.status);
+        go = __all_sync(0xffffffffu, ok);
+        if (!go) {
+          if (lane == 0) raise_peer();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + acc * ACC_COLS;
+        if (MODE == ROWS) {
+          // block: lanes = features r0.., columns = tokens; stored transposed
+          O* const out = reinterpret_cast<O*>(p.out);
+          for (int c = half * 32; c < t.nvalid; c += 64) {
+            if (r0 >= p.M) break;  // warp-uniform
+            uint32_t f0[16], f1[16];
+            tmem_ld_16x256_x4(trow + c, f0);
+            tmem_ld_16x256_x4(trow + c + (16u << 16), f1);
+            tmem_wait_ld();
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int x = 4 * i + 2 * k;
+                pk[4 * k + i] = Elem<T>::pack2(__uint_as_float(f0[x]), __uint_as_float(f0[x + 1]));
+                pk[8 + 4 * k + i] = Elem<T>::pack2(__uint_as_float(f1[x]), __uint_as_float(f1[x + 1]));
+              }
+            __syncwarp();  // the previous chunk has been read
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              stsm_x4_trans(sd_a + sw64(lane, 16 * (k >> 1) + 8 * (k & 1)), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2],
+                            pk[4 * k + 3]);
             __syncwarp();
-            const int x0 = (lane & 3) * 8;
+            // rows of 32 features: four lanes a row, 16 bytes a lane
+            const int f = r0 + (lane & 3) * 8;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int r = 8 * j + (lane >> 2);
-              if (r >= rows || x0 >= cols) continue;
-              const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(r, x0));
-              O* d = out + (wr + r) * ldo + c + x0;
-              if (x0 + 8 <= cols) {
+              const int tk = 8 * j + (lane >> 2);
+              if (c + tk >= t.nvalid || f >= p.M) continue;
+              const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(tk, (lane & 3) * 8));
+              O* d = out + (long long)(t.n0 + c + tk) * p.ldo + f;
+              if (f + 8 <= p.M) {
                 *reinterpret_cast<uint4*>(d) = v;
               } else {
                 const O* h = reinterpret_cast<const O*>(&v);
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                  if (x0 + x < cols) d[x] = h[x];
+                  if (f + x < p.M) d[x] = h[x];
               }
             }
-            continue;
           }
-          const int cc = (lane & 7) * 4;
-          O* const at = out + (wr + (lane >> 3)) * ldo + c + cc;  // row 4 j + lane / 8 at at + 4 j ldo
-          // what is added to: this chunk's was loaded while the one before was
-          // worked on (the first chunk's before the accumulator was waited for)
-          float4 old[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) old[j] = ahead[j];
-          if (beta != 0.f && c + 64 < NT) load_old(c + 64);
-          uint32_t raw[32];
-          if (t.nkb > 0) {
-            tmem_ld_32x32(trow + c, raw);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) raw[x] = 0u;
-          }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(sd + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                make_uint4(raw[4 * k], raw[4 * k + 1], raw[4 * k + 2], raw[4 * k + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int rr = 4 * j + (lane >> 3);
-            if (rr >= rows || cc >= cols) continue;
-            float4 v = *reinterpret_cast<const float4*>(sd + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-            v.x *= p.alpha; v.y *= p.alpha; v.z *= p.alpha; v.w *= p.alpha;
-            if (beta != 0.f) {
-              v.x = fmaf(beta, old[j].x, v.x); v.y = fmaf(beta, old[j].y, v.y);
-              v.z = fmaf(beta, old[j].z, v.z); v.w = fmaf(beta, old[j].w, v.w);
+        } else {
+          // block: lanes = rows of dW_e, columns = its columns; staged so that
+          // neighbouring lanes hold neighbouring columns. A part of a tile goes
+          // to its 256 x 256 place in the workspace (none when it has no rows).
+          const bool skip = !t.whole && t.nkb == 0;
+          O* const out = t.whole ? reinterpret_cast<O*>(p.out) + (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0
+                                 : reinterpret_cast<O*>(p.partial) + (long long)tile * (TILE_M * NT);
+          const long long ldo = t.whole ? p.ldo : NT;
+          const int rows = skip ? 0 : min(p.M - r0, 32), wr = r0 - t.m0;  // rows of this warp, from row wr of the tile
+          for (int c = half * 32; c < NT; c += 64) {
+            const int cols = p.N - t.n0 - c;
+            if (rows <= 0 || cols <= 0) break;  // warp-uniform
+            if (t.nkb == 0 && beta == 0.f) {
+              constexpr int V = 16 / sizeof(O);  // no rows, nothing to add to: zeros
+              for (int i = lane; i < rows * (32 / V); i += 32) {
+                const int r = i / (32 / V), x0 = (i % (32 / V)) * V;
+                O* d = out + (wr + r) * ldo + c + x0;
+                if (x0 + V <= cols) *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
+                else
+                  for (int x = 0; x < V; ++x)
+                    if (x0 + x < cols) d[x] = f_to_out<O>(0.f);
+              }
+              continue;
             }
-            O* d = at + 4 * j * ldo;
-            if (cc + 4 <= cols) {
-              store_out4<O>(d, v);
-            } else {
-              const float* o = &v.x;
+            if (!std::is_same<O, float>::value && beta == 0.f) {
+              // 16-bit result alone: rounded before it is staged, four lanes a row
+              uint32_t raw[32];
+              tmem_ld_32x32(trow + c, raw);
+              tmem_wait_ld();
+              __syncwarp();
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (cc + x < cols) d[x] = f_to_out<O>(o[x]);
+              for (int k = 0; k < 4; ++k) {
+                uint32_t h[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  h[x] = Elem<T>::pack2(p.alpha * __uint_as_float(raw[8 * k + 2 * x]), p.alpha * __uint_as_float(raw[8 * k + 2 * x + 1]));
+                *reinterpret_cast<uint4*>(sd + sw64(lane, 8 * k)) = make_uint4(h[0], h[1], h[2], h[3]);
+              }
+              __syncwarp();
+              const int x0 = (lane & 3) * 8;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = 8 * j + (lane >> 2);
+                if (r >= rows || x0 >= cols) continue;
+                const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(r, x0));
+                O* d = out + (wr + r) * ldo + c + x0;
+                if (x0 + 8 <= cols) {
+                  *reinterpret_cast<uint4*>(d) = v;
+                } else {
+                  const O* h = reinterpret_cast<const O*>(&v);
+#pragma unroll
+                  for (int x = 0; x < 8; ++x)
+                    if (x0 + x < cols) d[x] = h[x];
+                }
+              }
+              continue;
+            }
+            const int cc = (lane & 7) * 4;
+            O* const at = out + (wr + (lane >> 3)) * ldo + c + cc;  // row 4 j + lane / 8 at at + 4 j ldo
+            // what is added to: this chunk's was loaded while the one before was
+            // worked on (the first chunk's before the accumulator was waited for)
+            float4 old[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) old[j] = ahead[j];
+            if (beta != 0.f && c + 64 < NT) load_old(c + 64);
+            uint32_t raw[32];
+            if (t.nkb > 0) {
+              tmem_ld_32x32(trow + c, raw);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; ++x) raw[x] = 0u;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(sd + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                  make_uint4(raw[4 * k], raw[4 * k + 1], raw[4 * k + 2], raw[4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int rr = 4 * j + (lane >> 3);
+              if (rr >= rows || cc >= cols) continue;
+              float4 v = *reinterpret_cast<const float4*>(sd + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+              v.x *= p.alpha; v.y *= p.alpha; v.z *= p.alpha; v.w *= p.alpha;
+              if (beta != 0.f) {
+                v.x = fmaf(beta, old[j].x, v.x); v.y = fmaf(beta, old[j].y, v.y);
+                v.z = fmaf(beta, old[j].z, v.z); v.w = fmaf(beta, old[j].w, v.w);
+              }
+              O* d = at + 4 * j * ldo;
+              if (cc + 4 <= cols) {
+                store_out4<O>(d, v);
+              } else {
+                const float* o = &v.x;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  if (cc + x < cols) d[x] = f_to_out<O>(o[x]);
+              }
             }
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank != 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
-        else mbar_arrive(&tempty[acc]);
-      }
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
-      }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank != 0) mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+          else mbar_arrive(&tempty[acc]);
+        }
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
       }
     }
   }

