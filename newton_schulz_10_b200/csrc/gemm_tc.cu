@@ -13,8 +13,9 @@
 //             leader's barrier. MMA completions are signalled to both CTAs'
 //             barriers.
 // Roles:
-//   warps 0, 3  TMA producers (one thread each: A boxes, B boxes), 128-byte swizzle
-//   warp 1      MMA issuer (one thread of the leader), fp32 accumulators in TMEM
+//   warps 0, 3  TMA producers (A boxes, B boxes), 128-byte swizzle
+//   warp 1      MMA issuer (of the leader), fp32 accumulators in TMEM
+//               (converged warps, one elected lane issuing: see common.cuh)
 //   warp 2      allocates / frees the 512 TMEM columns (two 128xBN fp32
 //               accumulators: the epilogue of tile i overlaps the mainloop of
 //               tile i+1)
@@ -387,11 +388,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t budget = p.timeout_ns;
 
-  if ((warp == 0 || warp == 3) && lane == 0) {
+  if (warp == 0 || warp == 3) {
+    const uint32_t on = elect_one();  // the lane that waits for dependencies and issues
     // ------------------------------------------------------------------
-    // TMA producers (each CTA loads its own halves). Issuing a tensor copy
-    // costs the issuing thread hundreds of cycles, so two threads in
-    // different warps issue in parallel: warp 0 the A boxes (and the
+    // TMA producers (each CTA loads its own halves). Two warps issue in
+    // parallel: warp 0 the A boxes (and the
     // leader's byte count), warp 3 the B boxes. Each of them has a box in
     // every k-block, so no stage phase can complete without both, and
     // neither can fall two phases behind the parity it waits on.
@@ -415,13 +416,17 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
       const int bn0 = t.n0 + (int)rank * (BN / PAIR);   // this CTA's rows of B
       bool ok = true;
       if (g.dep >= 0) {
-        if (next_ctr == p.counters + g.dep + t.b && next_val >= g.dep_target) {
-          fence_acquire_gpu();
-          fence_proxy_async_global();
-        } else if (!wait_dep(p, g, t.b, abort_flag, budget)) {
-          raise_peer();
-          break;
+        if (on) {
+          if (next_ctr == p.counters + g.dep + t.b && next_val >= g.dep_target) {
+            fence_acquire_gpu();
+            fence_proxy_async_global();
+          } else if (!wait_dep(p, g, t.b, abort_flag, budget)) {
+            raise_peer();
+            ok = false;
+          }
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
       }
       next_ctr = nullptr;
       if (tile + units < p.total_tiles) {
@@ -429,22 +434,22 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         const Job& gn = p.g[tn.g];
         if (gn.dep >= 0) {
           next_ctr = p.counters + gn.dep + tn.b;
-          next_val = ld_relaxed_gpu(next_ctr);
+          if (on) next_val = ld_relaxed_gpu(next_ctr);
         }
       }
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status)) {
-          raise_peer();
-          ok = false;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status));
+        if (!ok) {
+          if (on) raise_peer();
           break;
         }
-        if (issues_a && rank == 0) mbar_arrive_expect_tx(&full[stage], Cf::TX_BYTES);
+        if (issues_a && rank == 0) mbar_arrive_expect_tx_if(on, &full[stage], Cf::TX_BYTES);
         uint8_t* a = sA + stage * Cf::A_STAGE;
         uint8_t* b = sB + stage * Cf::B_STAGE;
         const int k0 = kb * BK;
         auto load = [&](void* dst, const CUtensorMap* m, int c0, int c1) {
-          if (PAIR == 2) tma_load_3d_pair(dst, m, c0, c1, t.b * PL, &full[stage]);
-          else tma_load_3d(dst, m, c0, c1, t.b * PL, &full[stage]);
+          if (PAIR == 2) tma_load_3d_pair_if(on, dst, m, c0, c1, t.b * PL, &full[stage]);
+          else tma_load_3d_if(on, dst, m, c0, c1, t.b * PL, &full[stage]);
         };
         if (issues_a) {
           if (!g.a_mn) {
@@ -485,12 +490,13 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
       // leader settles and drains those barriers after the final cluster
       // barrier (settle_pair_copies).
       const uint32_t slot = smem_u32(const_cast<int*>(issued_cnt + 2 * rank + (issues_a ? 0 : 1)));
-      st_cluster_u32(mapa_shared(slot, 0), (uint32_t)issued);
+      if (on) st_cluster_u32(mapa_shared(slot, 0), (uint32_t)issued);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------------
     // MMA issuer (the leader issues for the pair)
     // ------------------------------------------------------------------
+    const uint32_t on = elect_one();
     int stage = 0;
     uint32_t phase = 0;
     int acc = 0;
@@ -516,16 +522,17 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
       // descriptor fields other than the start address, fixed for the tile;
       // start addresses (>> 4) stay below 2^14 inside the 228 KB window
       const uint64_t a_hi = smem_desc_sw128(0, a_lbo, 1024), b_hi = smem_desc_sw128(0, b_lbo, 1024);
-      if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, budget, p.status)) {
-        raise_peer();
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, abort_flag, budget, p.status));
+      if (!ok) {
+        if (on) raise_peer();
         break;
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * BN;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, budget, p.status)) {
-          raise_peer();
-          ok = false;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, abort_flag, budget, p.status));
+        if (!ok) {
+          if (on) raise_peer();
           break;
         }
         // No tcgen05 fence here: the stage barrier completes only when the
@@ -537,20 +544,20 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
           const uint64_t ad = a_hi | (uint64_t)(a_lo + k * (a_kstep >> 4));
           const uint64_t bd = b_hi | (uint64_t)(b_lo + k * (b_kstep >> 4));
           const bool accumulate = kb != t.kb0 || k != 0;
-          if (PAIR == 2) umma_f16_pair(d_tmem, ad, bd, idesc, accumulate);
-          else umma_f16(d_tmem, ad, bd, idesc, accumulate);
+          if (PAIR == 2) umma_f16_pair_if(on, d_tmem, ad, bd, idesc, accumulate);
+          else umma_f16_if(on, d_tmem, ad, bd, idesc, accumulate);
           if (PL == 2) {
             if (PAIR == 2) {
-              umma_f16_pair(d_tmem, ad, bd + b_low, idesc, true);
-              umma_f16_pair(d_tmem, ad + a_low, bd, idesc, true);
+              umma_f16_pair_if(on, d_tmem, ad, bd + b_low, idesc, true);
+              umma_f16_pair_if(on, d_tmem, ad + a_low, bd, idesc, true);
             } else {
-              umma_f16(d_tmem, ad, bd + b_low, idesc, true);
-              umma_f16(d_tmem, ad + a_low, bd, idesc, true);
+              umma_f16_if(on, d_tmem, ad, bd + b_low, idesc, true);
+              umma_f16_if(on, d_tmem, ad + a_low, bd, idesc, true);
             }
           }
         }
         // frees the stage (in both CTAs) once these MMAs have read it
-        if (PAIR == 2) umma_commit_pair(&empty[stage], 0x3); else umma_commit(&empty[stage]);
+        if (PAIR == 2) umma_commit_pair_if(on, &empty[stage], 0x3); else umma_commit_if(on, &empty[stage]);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
       }
       if (!ok) break;
       // accumulator ready for the epilogue (of both CTAs)
-      if (PAIR == 2) umma_commit_pair(&tfull[acc], 0x3); else umma_commit(&tfull[acc]);
+      if (PAIR == 2) umma_commit_pair_if(on, &tfull[acc], 0x3); else umma_commit_if(on, &tfull[acc]);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1;
@@ -566,9 +573,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     }
     // Drain: every MMA issued completes (and every earlier completion signal
     // has arrived) before TMEM is freed.
-    if (PAIR == 2) umma_commit_pair(drain, 0x3); else umma_commit(drain);
+    if (PAIR == 2) umma_commit_pair_if(on, drain, 0x3); else umma_commit_if(on, drain);
     drain_wait(drain, 0, p.status);
-  } else if (PAIR == 2 && warp == 1 && lane == 0) {
+  } else if (PAIR == 2 && warp == 1) {
     // the follower learns from the leader's drain signal that no MMA still
     // reads its shared memory or writes its TMEM
     drain_wait(drain, 0, p.status);
