@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   const uint32_t idesc_n = idesc_f16(fmt, 0, 0, 128, p.np), idesc_x = idesc_f16(fmt, 0, 1, 128, mc);
   uint32_t parity = 0;
   // after the operands are written: order them before the products, which
-  // thread 0 issues, and wait for their completion. A wait that runs out
+  // warp 0 issues, and wait for their completion. A wait that runs out
   // reports it and then still waits, with the drain's bound, so that nothing
   // reads, overwrites or frees what a product in flight uses; the cluster's
   // barriers need every CTA, so the chain goes on.
@@ -367,10 +367,11 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     fence_operands();
     tc_fence_before();
     __syncthreads();
-    if (tid == 0) {
+    if (warp == 0) {
       tc_fence_after();
-      issue();
-      umma_commit(bar);
+      const uint32_t on = elect_one();
+      issue(on);
+      umma_commit_if(on, bar);
     }
     wait_for(bar, parity);
     parity ^= 1;
@@ -378,10 +379,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     tc_fence_after();
   };
   // hi hi, + hi lo where the N side has two planes, + lo hi where the M side has
-  auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t low_a, uint32_t low_b, uint32_t idesc, bool acc) {
-    umma_f16(d, ad, bd, idesc, acc);
-    if (low_b) umma_f16(d, ad, bd + low_b, idesc, 1);
-    if (low_a) umma_f16(d, ad + low_a, bd, idesc, 1);
+  auto mma = [&](uint32_t on, uint32_t d, uint64_t ad, uint64_t bd, uint32_t low_a, uint32_t low_b, uint32_t idesc, bool acc) {
+    umma_f16_if(on, d, ad, bd, idesc, acc);
+    if (low_b) umma_f16_if(on, d, ad, bd + low_b, idesc, 1);
+    if (low_a) umma_f16_if(on, d, ad + low_a, bd, idesc, 1);
   };
   const int q = warp & 3, half = warp >> 2;
   const int row = q * 32 + lane;                 // this thread's accumulator lane
@@ -407,12 +408,12 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     const float lin = p.lin[t], quad = p.quad[t], diag = p.diag[t], alpha = p.alpha;
     const uint32_t odd = (uint32_t)t & 1u;  // phase of the exchange's barriers
     // A = X X^T over this CTA's columns
-    products([&]() {
+    products([&](uint32_t on) {
       for (int j = 0; j < g; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint64_t d = k_major | (uint64_t)((x_d + j * GROUP + k * 32) >> 4);
-          mma(tmem, d, d, x_low, x_low, idesc_n, j != 0 || k != 0);
+          mma(on, tmem, d, d, x_low, x_low, idesc_n, j != 0 || k != 0);
         }
     });
     if (rows_here) {
@@ -500,10 +501,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       wait_for(rows, odd);
     }
     // B' = a I + b A + c A A, in A's place (every thread rewrites what it read)
-    products([&]() {
+    products([&](uint32_t on) {
       for (int k = 0; k < p.np / 16; ++k) {
         const uint64_t d = k_major | (uint64_t)((a_d + (k >> 2) * GROUP + (k & 3) * 32) >> 4);
-        mma(tmem, d, d, a_low, a_low, idesc_n, k != 0);
+        mma(on, tmem, d, d, a_low, a_low, idesc_n, k != 0);
       }
     });
     if (rows_here) {
@@ -529,11 +530,11 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       }
     }
     // X <- B' X
-    products([&]() {
+    products([&](uint32_t on) {
       for (int k = 0; k < p.np / 16; ++k) {
         const uint64_t ad = k_major | (uint64_t)((a_d + (k >> 2) * GROUP + (k & 3) * 32) >> 4);
         const uint64_t bd = mn_major | (uint64_t)((x_d + k * 2048) >> 4);
-        mma(tmem + X_COL, ad, bd, a_low, x_low, idesc_x, k != 0);
+        mma(on, tmem + X_COL, ad, bd, a_low, x_low, idesc_x, k != 0);
       }
     });
     const bool last = t + 1 == p.T;
