@@ -35,8 +35,7 @@
 // The issuing roles are whole warps (common.cuh: 491 -> 444 us for 32768 rows
 // of 2048 into 64 x 4096). An operand is one copy per k-block (an MN-major
 // one, 64 columns wide by its swizzle, through a map that has the 64-column
-// blocks as a dimension of their own), and two warps take turns with the M
-// side, which alone decides how fast a launch of a few tiles streams weights.
+// blocks as a dimension of their own).
 //
 // Every wait is bounded as in the Newton-Schulz GEMM; offsets are clamped to
 // 0..tokens before use, and a decreasing or out-of-range entry is reported as
@@ -79,7 +78,6 @@ struct Cfg {
   static constexpr int B_STAGE = (NT / 2) * BK * 2;
   static constexpr int TX_BYTES = 2 * (A_STAGE + B_STAGE);  // per stage, both CTAs
   static constexpr int STAGES = NT == 256 ? 6 : NT <= 64 ? 10 : 8;
-  static_assert(STAGES % 2 == 0, "each of the two M-side producers keeps its stages");
   static constexpr int EPI_BUF = MODE == ROWS ? 2048 : 4096;  // one 32x32 block per warp (16-bit, fp32)
   static constexpr int TABLE = MODE == ROWS ? (kMaxExperts + 1 + 32) * 4 : 0;
   static constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * EPI_BUF + TABLE + (2 * STAGES + 5) * 8 + 64;
@@ -205,30 +203,23 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* 
 }
 
 // Early exit of a pair: wait until every operand copy that either CTA issued
-// has landed. cnt: k-blocks issued by each CTA's producers (M side of even
-// and of odd k-blocks, N side; the leader's, then the follower's). Blocks
-// STAGES before the last one issued have been consumed; each later one
-// occupies its own stage, whose barrier is settled for the copies that were
-// never issued and then waited on.
+// has landed. cnt: k-blocks issued by the leader's M-side and N-side producer
+// and the follower's. Blocks before max(cnt) - STAGES have been consumed;
+// each later one occupies its own stage, whose barrier is settled for the
+// copies that were never issued and then waited on.
 template <int MODE, int NT>
 __device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
   using Cf = Cfg<MODE, NT>;
-  // whether producer x (0, 1: M side, 2: N side; + 3: the follower's) issued block j
-  auto has = [&](int x, int j) {
-    const int kind = x % 3;
-    return kind == 2 ? j < cnt[x] : (j & 1) == kind && (j >> 1) < cnt[x];
-  };
+  const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
+  const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
   int hi = 0;
-  for (int x = 0; x < 6; ++x) {
-    const int kind = x % 3, last = kind == 2 ? cnt[x] : cnt[x] > 0 ? 2 * (cnt[x] - 1) + kind + 1 : 0;
-    hi = last > hi ? last : hi;
-  }
+  for (int x = 0; x < 4; ++x) hi = c[x] > hi ? c[x] : hi;
   for (int j = hi > Cf::STAGES ? hi - Cf::STAGES : 0; j < hi; ++j) {
     uint32_t issued = 0;
-    for (int x = 0; x < 6; ++x)
-      if (has(x, j)) issued += x % 3 == 2 ? Cf::B_STAGE : Cf::A_STAGE;
+    for (int x = 0; x < 4; ++x)
+      if (j < c[x]) issued += bytes[x];
     uint64_t* bar = &full[j % Cf::STAGES];
-    if (has(j & 1, j)) {
+    if (j < c[0]) {
       if (issued < (uint32_t)Cf::TX_BYTES) mbar_complete_tx(bar, Cf::TX_BYTES - issued);
     } else {
       mbar_arrive_expect_tx(bar, issued);
@@ -245,6 +236,7 @@ __device__ __forceinline__ void fence_map_acquire(const CUtensorMap* m) {
 // count cut at the expert's last row.
 __global__ void __launch_bounds__(128) clip_maps(const __grid_constant__ Params p) {
   grid_dependency_wait();
+  grid_dependents_launch();  // the products' setup overlaps this launch; they wait for its end
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   const int e = i >> 1;
   if (e >= p.experts) return;
@@ -335,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
-    for (int i = 0; i < 6; ++i) issued_cnt[i] = 0;
+    for (int i = 0; i < 4; ++i) issued_cnt[i] = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -401,13 +393,11 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t budget = p.timeout_ns;
 
-  if (warp != 1 && warp < EPI_WARP0) {
+  if (warp == 0 || warp == 3) {
+    // TMA producers: warp 0 the M side (and the leader's byte count), warp 3
+    // the N side; both take part in every phase of every stage.
     const uint32_t on = elect_one();
-    // TMA producers: warps 0 and 2 the M side of even and odd k-blocks (and
-    // the leader's byte count), warp 3 the N side. STAGES is even, so each
-    // takes part in every phase of its stages.
-    const bool issues_a = warp != 3;
-    const int turn = warp >> 1;  // 0 or 1: the k-blocks (counted over all tiles) of an M-side producer
+    const bool issues_a = warp == 0;
     int stage = 0;
     uint32_t phase = 0;
     int issued = 0;
@@ -426,47 +416,45 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         }
       }
       for (int kb = 0; kb < t.nkb; ++kb) {
-        if (!issues_a || (stage & 1) == turn) {
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status)) {
-            if (on) raise_peer();
-            ok = false;
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (issues_a && rank == 0) mbar_arrive_expect_tx_if(on, &full[stage], Cf::TX_BYTES);
-          uint8_t* a = sA + stage * Cf::A_STAGE;
-          uint8_t* b = sB + stage * Cf::B_STAGE;
-          const int k0 = kb * BK;
-          if (MODE == ROWS) {
-            if (!issues_a) {
-              tma_load_3d_pair_if(on, b, map, k0, bn0, 0, &full[stage]);
-            } else if (!p.a_mn) {
-              tma_load_3d_pair_if(on, a, map, k0, am0, t.e, &full[stage]);
-            } else if (p.a_one) {
-              tma_load_4d_pair_if(on, a, map, 0, k0, am0 >> 6, t.e, &full[stage]);
-            } else {
-              tma_load_3d_pair_if(on, a, map, am0, k0, t.e, &full[stage]);
-              tma_load_3d_pair_if(on, a + 8192, map, am0 + 64, k0, t.e, &full[stage]);
-            }
-          } else {
-            uint8_t* d = issues_a ? a : b;
-            const int c0 = issues_a ? am0 : bn0;
-            if (issues_a ? p.a_one : p.b_one) {
-              tma_load_3d_pair_if(on, d, map, 0, t.t0 + k0, c0 >> 6, &full[stage]);
-            } else {
-              tma_load_3d_pair_if(on, d, map, c0, t.t0 + k0, 0, &full[stage]);
-              tma_load_3d_pair_if(on, d + 8192, map, c0 + 64, t.t0 + k0, 0, &full[stage]);
-            }
-          }
-          ++issued;
+        if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, budget, p.status)) {
+          if (on) raise_peer();
+          ok = false;
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (issues_a && rank == 0) mbar_arrive_expect_tx_if(on, &full[stage], Cf::TX_BYTES);
+        uint8_t* a = sA + stage * Cf::A_STAGE;
+        uint8_t* b = sB + stage * Cf::B_STAGE;
+        const int k0 = kb * BK;
+        if (MODE == ROWS) {
+          if (!issues_a) {
+            tma_load_3d_pair_if(on, b, map, k0, bn0, 0, &full[stage]);
+          } else if (!p.a_mn) {
+            tma_load_3d_pair_if(on, a, map, k0, am0, t.e, &full[stage]);
+          } else if (p.a_one) {
+            tma_load_4d_pair_if(on, a, map, 0, k0, am0 >> 6, t.e, &full[stage]);
+          } else {
+            tma_load_3d_pair_if(on, a, map, am0, k0, t.e, &full[stage]);
+            tma_load_3d_pair_if(on, a + 8192, map, am0 + 64, k0, t.e, &full[stage]);
+          }
+        } else {
+          uint8_t* d = issues_a ? a : b;
+          const int c0 = issues_a ? am0 : bn0;
+          if (issues_a ? p.a_one : p.b_one) {
+            tma_load_3d_pair_if(on, d, map, 0, t.t0 + k0, c0 >> 6, &full[stage]);
+          } else {
+            tma_load_3d_pair_if(on, d, map, c0, t.t0 + k0, 0, &full[stage]);
+            tma_load_3d_pair_if(on, d + 8192, map, c0 + 64, t.t0 + k0, 0, &full[stage]);
+          }
+        }
+        ++issued;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-    const uint32_t slot = smem_u32(const_cast<int*>(issued_cnt + 3 * rank + (issues_a ? turn : 2)));
+    const uint32_t slot = smem_u32(const_cast<int*>(issued_cnt + 2 * rank + (issues_a ? 0 : 1)));
     if (on) st_cluster_u32(mapa_shared(slot, 0), (uint32_t)issued);
   } else if (warp == 1 && rank == 0) {
     // MMA issuer (the leader issues for the pair)
@@ -744,6 +732,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
 template <typename O>
 __global__ void __launch_bounds__(256) add_parts(const __grid_constant__ Params p) {
   grid_dependency_wait();
+  grid_dependents_launch();
   const int q = (p.N + 3) / 4;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= (long long)p.experts * p.M * q) return;

@@ -44,6 +44,7 @@ template <int WG, typename T, bool CAST>
 __global__ void __launch_bounds__(BLOCK) stack_momentum(const __grid_constant__ StackLaunch L) {
   __shared__ double scratch[32];
   grid_dependency_wait();
+  grid_dependents_launch();
   const int task = blockIdx.x * (BLOCK / WG) + threadIdx.x / WG;
   const int l = threadIdx.x % WG;
   const bool active = task < L.total_rows;
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(BLOCK) stack_momentum(const __grid_constant__ 
 // with eps = 0); the scale of a norm below 1 / FLT_MAX is FLT_MAX.
 __global__ void __launch_bounds__(BLOCK) stack_norm(const __grid_constant__ StackLaunch L) {
   grid_dependency_wait();
+  grid_dependents_launch();
   const int i = blockIdx.x * (BLOCK / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= L.total_mats) return;
   int lo = 0, hi = L.count - 1;
@@ -133,6 +135,7 @@ __global__ void __launch_bounds__(BLOCK) stack_norm(const __grid_constant__ Stac
 template <int WG, typename T, int PL>
 __global__ void __launch_bounds__(BLOCK) stack_cast(const __grid_constant__ StackLaunch L) {
   grid_dependency_wait();
+  grid_dependents_launch();
   const int task = blockIdx.x * (BLOCK / WG) + threadIdx.x / WG;
   const int l = threadIdx.x % WG;
   if (task >= L.total_rows) return;
@@ -175,6 +178,7 @@ __global__ void __launch_bounds__(BLOCK) stack_cast(const __grid_constant__ Stac
 template <int WG, typename T, int PL>
 __global__ void __launch_bounds__(BLOCK) stack_update(const __grid_constant__ StackLaunch L) {
   grid_dependency_wait();
+  grid_dependents_launch();
   const int task = blockIdx.x * (BLOCK / WG) + threadIdx.x / WG;
   const int l = threadIdx.x % WG;
   if (task >= L.total_rows) return;
