@@ -1150,6 +1150,12 @@ bool make_tensor_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int6
   return make_map(m, t, base, inner, outer, batch, ld, bstride, box_outer);
 }
 
+bool make_block_store_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
+                          int64_t bstride) {
+  return make_map(m, t, base, inner, outer, batch, ld, bstride, 32, 32,
+                  t == Op::F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 bool make_block_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
                     int64_t bstride) {
   EncodeTiledFn enc = encode_fn();

@@ -72,15 +72,16 @@ constexpr int kPartBlocks = 12;
 
 enum : int { ROWS = 0, DW = 1 };
 
-template <int MODE, int NT>
+template <typename O, int MODE, int NT>
 struct Cfg {
   static constexpr int A_STAGE = BM * BK * 2;
   static constexpr int B_STAGE = (NT / 2) * BK * 2;
   static constexpr int TX_BYTES = 2 * (A_STAGE + B_STAGE);  // per stage, both CTAs
-  static constexpr int STAGES = NT == 256 ? 6 : NT <= 64 ? 10 : 8;
-  static constexpr int EPI_BUF = MODE == ROWS ? 2048 : 4096;  // one 32x32 block per warp (16-bit, fp32)
+  static constexpr int STAGES = MODE == DW && sizeof(O) == 4 ? 5 : NT == 256 ? 6 : NT <= 64 ? 10 : 8;
+  static constexpr int EPI_BLOCK = 32 * 32 * (int)sizeof(O);
+  static constexpr int EPI_BUF = MODE == ROWS ? EPI_BLOCK : 2 * EPI_BLOCK;  // per warp; DW: two, in turn
   static constexpr int TABLE = MODE == ROWS ? (kMaxExperts + 1 + 32) * 4 : 0;
-  static constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * EPI_BUF + TABLE + (2 * STAGES + 5) * 8 + 64;
+  static constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * EPI_BUF + TABLE + (2 * STAGES + 5 + 2 * EPI_WARPS) * 8 + 64;
   static_assert(SMEM <= 232448, "exceeds the opt-in shared memory of one sm_100 CTA");
 };
 
@@ -88,6 +89,7 @@ struct Params {
   CUtensorMap mapA;       // ROWS: W; DW: dy (the copies per expert are in `clipped`)
   CUtensorMap mapB;       // ROWS: x or dy; DW: x
   CUtensorMap* clipped;   // DW: [experts][2]
+  CUtensorMap mapO;       // DW: where the kernel's results go (dW, or the parts' sums), in 32 x 32 blocks
   const int32_t* offsets;
   void* out;
   long long ldo, so;      // row stride; DW: expert stride
@@ -98,6 +100,7 @@ struct Params {
   int splits;             // DW: parts of an expert's rows (1: none, results go to out)
   float* partial;         // DW, splits > 1: 256 x 256 fp32 per (tile, part)
   float alpha, beta;      // DW
+  int by_element;         // DW: rows end inside 16 bytes, which a bulk store would write whole
   int* status;
   unsigned long long timeout_ns;
 };
@@ -207,9 +210,9 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* 
 // and the follower's. Blocks before max(cnt) - STAGES have been consumed;
 // each later one occupies its own stage, whose barrier is settled for the
 // copies that were never issued and then waited on.
-template <int MODE, int NT>
+template <typename O, int MODE, int NT>
 __device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
-  using Cf = Cfg<MODE, NT>;
+  using Cf = Cfg<O, MODE, NT>;
   const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
   const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
   int hi = 0;
@@ -226,6 +229,25 @@ __device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int*
     }
     drain_wait(bar, (uint32_t)((j / Cf::STAGES) & 1), status);
   }
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// This thread's bulk stores: all but the last one (or all) have read their source; all have been written.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Sixteen bytes of row `lane` of a staged 32 x 32 block: chunk k, swizzled as
+// the block's tensor map has it (128-byte rows of fp32, 64-byte of 16 bits).
+template <typename O>
+__device__ __forceinline__ uint32_t block_at(int lane, int k) {
+  return sizeof(O) == 4 ? (uint32_t)(lane * 128 + ((k ^ (lane & 7)) << 4)) : (uint32_t)(lane * 64 + (((k ^ (lane >> 1)) & 3) << 4));
 }
 
 __device__ __forceinline__ void fence_map_acquire(const CUtensorMap* m) {
@@ -293,7 +315,7 @@ __device__ __forceinline__ void store_out4(O* p, float4 v) {
 
 template <typename T, typename O, int MODE, int NT>
 __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_constant__ Params p) {
-  using Cf = Cfg<MODE, NT>;
+  using Cf = Cfg<O, MODE, NT>;
   constexpr int STAGES = Cf::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -306,7 +328,8 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
   uint64_t* tfull = bars + 2 * STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* olds = drain + 1;        // DW: blocks to add to have arrived, two per epilogue warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(olds + 2 * EPI_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued_cnt = reinterpret_cast<volatile int*>(tmem_slot + 2);
   int* table = reinterpret_cast<int*>(tmem_slot + 8);  // ROWS: first token tile of each expert, then scan scratch
@@ -326,6 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       mbar_init(&tempty[b], EPI_WARPS * 2);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(&olds[i], 1);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) issued_cnt[i] = 0;
     fence_mbar_init();
@@ -524,6 +548,8 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     const uint32_t sd_a = smem_u32(sd);
     int acc = 0;
     uint32_t acc_phase = 0;
+    uint32_t old_phase = 0;  // DW: bit b is the parity of this warp's buffer b
+    uint32_t in_flight = 0;  // DW, lane 0: buffers whose block was asked for and not waited for
     bool go = true;
     for (int tile = unit; tile < total && go; tile += units) {
       const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
@@ -531,28 +557,24 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       for (int part = 0; part < parts; ++part) {
         const float beta = part == 0 ? p.beta : 1.f;
         const int r0 = t.m0 + (int)rank * BM + q * 32;  // first M-side row of this warp
-        float4 ahead[8];
-        // DW, beta: row 4 j + lane / 8, columns c + 4 (lane % 8).. of the block at column c
-        auto load_old = [&](int c) {
-          const O* d = reinterpret_cast<const O*>(t.whole ? p.out : p.partial) +
-                       (t.whole ? (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0 : (long long)tile * (TILE_M * NT));
-          const long long ldo = t.whole ? p.ldo : NT;
-          const int cols = p.N - t.n0 - c, rows = p.M - r0, cc = (lane & 7) * 4;
-          d += (r0 - t.m0 + (lane >> 3)) * ldo + c + cc;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (4 * j + (lane >> 3) >= rows || cc >= cols) continue;
-            if (cc + 4 <= cols) {
-              ahead[j] = load_out4<O>(d + 4 * j * ldo);
-            } else {
-              float* o = &ahead[j].x;
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (cc + x < cols) o[x] = out_to_f<O>(d[4 * j * ldo + x]);
-            }
-          }
+        // DW: this warp's 32 x 32 blocks (four, 64 columns apart) go through two
+        // buffers: what is added to arrives in one by a bulk copy while the
+        // other is worked on, the result replaces it and leaves by a bulk
+        // store. Rows and columns out of range are the copies' business.
+        const int rows = p.M - r0, z = t.whole ? t.e : tile;
+        const int row0 = t.whole ? r0 : r0 - t.m0, col0 = (t.whole ? t.n0 : 0) + half * 32;
+        const int blocks = MODE != DW || rows <= 0 || (!t.whole && t.nkb == 0) ? 0 : min(NT / 64, (p.N - t.n0 - half * 32 + 63) / 64);
+        const bool adds = MODE == DW && beta != 0.f;
+        auto ask = [&](int n) {  // lane 0; the buffer's last store has been read
+          mbar_arrive_expect_tx(&olds[2 * e + (n & 1)], Cf::EPI_BLOCK);
+          tma_load_3d(sd + (n & 1) * Cf::EPI_BLOCK, &p.mapO, col0 + 64 * n, row0, z, &olds[2 * e + (n & 1)]);
+          in_flight |= 1u << (n & 1);
         };
-        if (MODE == DW && beta != 0.f && (t.whole || t.nkb > 0)) load_old(half * 32);
+        if (adds && lane == 0) {
+          if (part > 0) bulk_wait0(); else bulk_wait_read0();  // a later part adds to what the last one stored
+          if (blocks > 0) ask(0);
+          if (blocks > 1) ask(1);
+        }
         const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, abort_flag, budget, p.status);
         go = __all_sync(0xffffffffu, ok);
         if (!go) {
@@ -604,105 +626,80 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
             }
           }
         } else {
-          // block: lanes = rows of dW_e, columns = its columns; staged so that
-          // neighbouring lanes hold neighbouring columns. A part of a tile goes
-          // to its 256 x 256 place in the workspace (none when it has no rows).
-          const bool skip = !t.whole && t.nkb == 0;
-          O* const out = t.whole ? reinterpret_cast<O*>(p.out) + (long long)t.e * p.so + (long long)t.m0 * p.ldo + t.n0
-                                 : reinterpret_cast<O*>(p.partial) + (long long)tile * (TILE_M * NT);
-          const long long ldo = t.whole ? p.ldo : NT;
-          const int rows = skip ? 0 : min(p.M - r0, 32), wr = r0 - t.m0;  // rows of this warp, from row wr of the tile
-          for (int c = half * 32; c < NT; c += 64) {
-            const int cols = p.N - t.n0 - c;
-            if (rows <= 0 || cols <= 0) break;  // warp-uniform
-            if (t.nkb == 0 && beta == 0.f) {
-              constexpr int V = 16 / sizeof(O);  // no rows, nothing to add to: zeros
-              for (int i = lane; i < rows * (32 / V); i += 32) {
-                const int r = i / (32 / V), x0 = (i % (32 / V)) * V;
-                O* d = out + (wr + r) * ldo + c + x0;
-                if (x0 + V <= cols) *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
-                else
-                  for (int x = 0; x < V; ++x)
-                    if (x0 + x < cols) d[x] = f_to_out<O>(0.f);
-              }
-              continue;
-            }
-            if (!std::is_same<O, float>::value && beta == 0.f) {
-              // 16-bit result alone: rounded before it is staged, four lanes a row
-              uint32_t raw[32];
-              tmem_ld_32x32(trow + c, raw);
-              tmem_wait_ld();
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t h[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  h[x] = Elem<T>::pack2(p.alpha * __uint_as_float(raw[8 * k + 2 * x]), p.alpha * __uint_as_float(raw[8 * k + 2 * x + 1]));
-                *reinterpret_cast<uint4*>(sd + sw64(lane, 8 * k)) = make_uint4(h[0], h[1], h[2], h[3]);
-              }
-              __syncwarp();
-              const int x0 = (lane & 3) * 8;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int r = 8 * j + (lane >> 2);
-                if (r >= rows || x0 >= cols) continue;
-                const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(r, x0));
-                O* d = out + (wr + r) * ldo + c + x0;
-                if (x0 + 8 <= cols) {
-                  *reinterpret_cast<uint4*>(d) = v;
-                } else {
-                  const O* h = reinterpret_cast<const O*>(&v);
-#pragma unroll
-                  for (int x = 0; x < 8; ++x)
-                    if (x0 + x < cols) d[x] = h[x];
-                }
-              }
-              continue;
-            }
-            const int cc = (lane & 7) * 4;
-            O* const at = out + (wr + (lane >> 3)) * ldo + c + cc;  // row 4 j + lane / 8 at at + 4 j ldo
-            // what is added to: this chunk's was loaded while the one before was
-            // worked on (the first chunk's before the accumulator was waited for)
-            float4 old[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) old[j] = ahead[j];
-            if (beta != 0.f && c + 64 < NT) load_old(c + 64);
+          // block: lanes = rows of dW_e (or of a part's 256 x 256), columns = its columns
+          for (int n = 0; n < blocks; ++n) {
+            uint8_t* const buf = sd + (n & 1) * Cf::EPI_BLOCK;
             uint32_t raw[32];
             if (t.nkb > 0) {
-              tmem_ld_32x32(trow + c, raw);
+              tmem_ld_32x32(trow + half * 32 + 64 * n, raw);
               tmem_wait_ld();
             } else {
 #pragma unroll
               for (int x = 0; x < 32; ++x) raw[x] = 0u;
             }
-            __syncwarp();
+            float v[32];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(sd + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                  make_uint4(raw[4 * k], raw[4 * k + 1], raw[4 * k + 2], raw[4 * k + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int rr = 4 * j + (lane >> 3);
-              if (rr >= rows || cc >= cols) continue;
-              float4 v = *reinterpret_cast<const float4*>(sd + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-              v.x *= p.alpha; v.y *= p.alpha; v.z *= p.alpha; v.w *= p.alpha;
-              if (beta != 0.f) {
-                v.x = fmaf(beta, old[j].x, v.x); v.y = fmaf(beta, old[j].y, v.y);
-                v.z = fmaf(beta, old[j].z, v.z); v.w = fmaf(beta, old[j].w, v.w);
+            for (int x = 0; x < 32; ++x) v[x] = p.alpha * __uint_as_float(raw[x]);
+            constexpr int V = 16 / sizeof(O);
+            if (adds) {
+              const uint32_t b = (uint32_t)(n & 1);
+              const bool here = mbar_wait_bounded(&olds[2 * e + b], (old_phase >> b) & 1, abort_flag, budget, p.status);
+              go = __all_sync(0xffffffffu, here);
+              if (!go) {
+                if (lane == 0) raise_peer();
+                break;
               }
-              O* d = at + 4 * j * ldo;
-              if (cc + 4 <= cols) {
-                store_out4<O>(d, v);
-              } else {
-                const float* o = &v.x;
+              old_phase ^= 1u << b;
+              in_flight &= ~(1u << b);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  if (cc + x < cols) d[x] = f_to_out<O>(o[x]);
+              for (int k = 0; k < 32 / V; ++k) {
+                const uint4 u = *reinterpret_cast<const uint4*>(buf + block_at<O>(lane, k));
+                const O* o = reinterpret_cast<const O*>(&u);
+#pragma unroll
+                for (int x = 0; x < V; ++x) v[V * k + x] = fmaf(beta, out_to_f<O>(o[x]), v[V * k + x]);
+              }
+            } else {
+              if (lane == 0) bulk_wait_read1();  // the store before last has read this buffer
+              __syncwarp();
+            }
+#pragma unroll
+            for (int k = 0; k < 32 / V; ++k) {
+              uint4 u;
+              O* o = reinterpret_cast<O*>(&u);
+#pragma unroll
+              for (int x = 0; x < V; ++x) o[x] = f_to_out<O>(v[V * k + x]);
+              *reinterpret_cast<uint4*>(buf + block_at<O>(lane, k)) = u;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (adds && n > 0 && n + 1 < blocks) {
+                bulk_wait_read0();  // the other buffer's store
+                ask(n + 1);
+              }
+              if (!p.by_element) {
+                tma_store_3d(&p.mapO, smem_u32(buf), col0 + 64 * n, row0, z);
+                bulk_commit();
               }
             }
+            if (p.by_element) {
+              O* const out = reinterpret_cast<O*>(p.out) + (long long)z * p.so + (long long)row0 * p.ldo + col0 + 64 * n;
+              const int cols = p.N - col0 - 64 * n;
+              for (int i = lane; i < 32 * (32 / V); i += 32) {
+                const int r = i / (32 / V), k = i % (32 / V);
+                if (r >= rows || V * k >= cols) continue;
+                const uint4 u = *reinterpret_cast<const uint4*>(buf + block_at<O>(r, k));
+                const O* o = reinterpret_cast<const O*>(&u);
+                O* d = out + (long long)r * p.ldo + V * k;
+                if (V * k + V <= cols) *reinterpret_cast<uint4*>(d) = u;
+                else
+                  for (int x = 0; V * k + x < cols; ++x) d[x] = o[x];
+              }
+              asm volatile("fence.proxy.async;" ::: "memory");  // a later part reads this by bulk copies
+              __syncwarp();
+            }
           }
+          if (!go) break;
         }
         tc_fence_before();
         __syncwarp();
@@ -716,13 +713,17 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         }
       }
     }
+    if (MODE == DW && lane == 0)  // after an early stop: no copy still writes here
+      for (int b = 0; b < 2; ++b)
+        if ((in_flight >> b) & 1) drain_wait(&olds[2 * e + b], (old_phase >> b) & 1, p.status);
   }
 
+  if (MODE == DW && warp >= EPI_WARP0 && lane == 0) bulk_wait0();  // every block is stored
   tc_fence_before();
   __syncwarp();
   cluster_sync();  // no CTA leaves while its pair still signals it
   tc_fence_after();
-  if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<MODE, NT>(full, issued_cnt, p.status);
+  if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<O, MODE, NT>(full, issued_cnt, p.status);
   __syncwarp();
   cluster_sync();
   if (warp == 2) tmem_dealloc_pair(tmem_base, TMEM_COLS);
@@ -784,7 +785,7 @@ int pair_units() {
   int& units = per_device[dev];
   if (units == 0) {
     const void* fn = (const void*)grp::grouped_kernel<T, O, MODE, NT>;
-    constexpr int smem = grp::Cfg<MODE, NT>::SMEM;
+    constexpr int smem = grp::Cfg<O, MODE, NT>::SMEM;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
       cudaGetLastError();
       return 0;
@@ -817,7 +818,7 @@ muon_status launch_grouped(const grp::Params& p, long long tiles, cudaStream_t s
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * use);
   cfg.blockDim = dim3(grp::THREADS);
-  cfg.dynamicSmemBytes = grp::Cfg<MODE, NT>::SMEM;
+  cfg.dynamicSmemBytes = grp::Cfg<O, MODE, NT>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -866,7 +867,7 @@ constexpr int kMinPartBlocks = 4;
 constexpr int kMaxParts = 16;
 
 template <typename T, typename O>
-muon_status dw_typed(grp::Params& p, cudaStream_t s) {
+muon_status dw_typed(grp::Params& p, Op out, cudaStream_t s) {
   muon_status r = launch_plain(grp::clip_maps, (2 * p.experts + 127) / 128, 128, p, s);
   if (r != MUON_OK) return r;
   const long long mt = (p.M + grp::TILE_M - 1) / grp::TILE_M, nt = (p.N + 255) / 256, tiles = mt * nt * p.experts;
@@ -875,8 +876,13 @@ muon_status dw_typed(grp::Params& p, cudaStream_t s) {
   long long parts = units / tiles;
   parts = std::min(parts, (long long)p.tokens / p.experts / (64 * kMinPartBlocks));
   p.splits = (int)std::max(1ll, std::min(parts, (long long)kMaxParts));
-  if (p.splits == 1) return launch_grouped<T, O, grp::DW, 256>(p, tiles, s);
+  if (p.splits == 1) {
+    p.by_element = p.N * (int)sizeof(O) % 16 != 0;
+    if (!make_block_store_map(&p.mapO, out, p.out, p.N, p.M, p.experts, p.ldo, p.so)) return MUON_ERR_CUDA;
+    return launch_grouped<T, O, grp::DW, 256>(p, tiles, s);
+  }
   grp::Params q = p;
+  if (!make_block_store_map(&q.mapO, Op::F32, p.partial, 256, grp::TILE_M, tiles * p.splits, 256, grp::TILE_M * 256)) return MUON_ERR_CUDA;
   q.alpha = 1.f;
   q.beta = 0.f;
   r = launch_grouped<T, float, grp::DW, 256>(q, tiles * p.splits, s);
@@ -968,8 +974,8 @@ muon_status grouped_dw(const GroupedDesc& g, const void* dy, const void* x, void
   p.status = g.status;
   p.timeout_ns = timeout_ns;
   if (g.type == Op::BF16)
-    return out == Op::F32 ? dw_typed<__nv_bfloat16, float>(p, s) : dw_typed<__nv_bfloat16, __nv_bfloat16>(p, s);
-  return out == Op::F32 ? dw_typed<__half, float>(p, s) : dw_typed<__half, __half>(p, s);
+    return out == Op::F32 ? dw_typed<__nv_bfloat16, float>(p, out, s) : dw_typed<__nv_bfloat16, __nv_bfloat16>(p, out, s);
+  return out == Op::F32 ? dw_typed<__half, float>(p, out, s) : dw_typed<__half, __half>(p, out, s);
 }
 
 }  // namespace muon

@@ -90,6 +90,10 @@ int num_sms();
 bool make_tensor_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
                      int64_t bstride, int box_outer);
 
+// The same with box {32, 32, 1}, swizzled by the block's row width (64 or 128
+// bytes): blocks of results.
+bool make_block_store_map(CUtensorMap* m, Op t, const void* base, int64_t inner, int64_t outer, int64_t batch, int64_t ld,
+                          int64_t bstride);
 // The same memory for MN-major operands whose width `inner` is a multiple of
 // 64: [batch][inner / 64][outer][64], box {64, 64, 2, 1}, so that one copy
 // brings two 64-column blocks of 64 rows (8 KB each, one after the other).
