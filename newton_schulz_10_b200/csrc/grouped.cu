@@ -80,7 +80,7 @@ struct Cfg {
   static constexpr int STAGES = MODE == DW && sizeof(O) == 4 ? 5 : NT == 256 ? 6 : NT <= 64 ? 10 : 8;
   static constexpr int EPI_BLOCK = 32 * 32 * (int)sizeof(O);
   static constexpr int EPI_BUF = MODE == ROWS ? EPI_BLOCK : 2 * EPI_BLOCK;  // per warp; DW: two, in turn
-  static constexpr int TABLE = MODE == ROWS ? (kMaxExperts + 1 + 32) * 4 : 0;
+  static constexpr int TABLE = MODE == ROWS ? (2 * kMaxExperts + 1 + 32) * 4 : 0;
   static constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * EPI_BUF + TABLE + (2 * STAGES + 5 + 2 * EPI_WARPS) * 8 + 64;
   static_assert(SMEM <= 232448, "exceeds the opt-in shared memory of one sm_100 CTA");
 };
@@ -95,6 +95,7 @@ struct Params {
   long long ldo, so;      // row stride; DW: expert stride
   int tokens, experts;
   int M, N, K;            // ROWS: M = features out, K = features in; DW: M = n, N = k
+  unsigned mt_inverse;    // ROWS: 2^32 / (tiles of the M side), rounded up
   int a_mn;               // ROWS: W read MN-major
   int a_one, b_one;       // an MN-major operand's boxes are one copy (its width is a multiple of 64)
   int splits;             // DW: parts of an expert's rows (1: none, results go to out)
@@ -136,15 +137,17 @@ template <int NT>
 __device__ __forceinline__ int token_tiles(int cnt) { return (cnt + NT - 1) / NT; }
 template <int NT>
 __device__ __forceinline__ int token_width(int cnt, int tiles) {
-  if (tiles > 4) return NT;
-  return ((cnt + tiles - 1) / tiles + 31) & ~31;
+  const int share = tiles <= 1 ? cnt : tiles == 2 ? (cnt + 1) >> 1 : tiles == 3 ? (cnt + 2) / 3 : (cnt + 3) >> 2;
+  return tiles > 4 ? NT : (share + 31) & ~31;
 }
 
 template <int MODE, int NT>
 __device__ __forceinline__ Tile decode(const Params& p, const int* tile_begin, int tile, int mt, int ntl) {
   Tile t;
   if (MODE == ROWS) {
-    const int tt = tile / mt;
+    // tile / mt by a multiplication with the inverse rounded up: one too large at most
+    int tt = mt == 1 ? tile : (int)(((unsigned long long)(unsigned)tile * p.mt_inverse) >> 32);
+    if (tt * mt > tile) --tt;
     t.m0 = (tile - tt * mt) * TILE_M;
     int lo = 0, hi = p.experts - 1;  // the last expert whose first token tile is <= tt
     while (lo < hi) {
@@ -152,11 +155,12 @@ __device__ __forceinline__ Tile decode(const Params& p, const int* tile_begin, i
       if (tile_begin[mid] <= tt) lo = mid; else hi = mid - 1;
     }
     t.e = lo;
-    const Span s = span_of(p, lo);
-    const int cnt = s.end - s.begin, tiles = token_tiles<NT>(cnt);
+    const int* const first = tile_begin + kMaxExperts;  // the offsets, clamped
+    const int begin = first[lo], end = max(begin, first[lo + 1]);
+    const int cnt = end - begin, tiles = token_tiles<NT>(cnt);
     const int w = token_width<NT>(cnt, tiles);
-    t.n0 = s.begin + (tt - tile_begin[lo]) * w;
-    const int left = s.end - t.n0;
+    t.n0 = begin + (tt - tile_begin[lo]) * w;
+    const int left = end - t.n0;
     t.nvalid = left < w ? left : w;
     t.n_mma = (t.nvalid + 31) & ~31;
     t.t0 = 0;
@@ -332,7 +336,8 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(olds + 2 * EPI_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued_cnt = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  int* table = reinterpret_cast<int*>(tmem_slot + 8);  // ROWS: first token tile of each expert, then scan scratch
+  // ROWS: first token tile of each expert, the experts' first rows (and the end), then scan scratch
+  int* table = reinterpret_cast<int*>(tmem_slot + 8);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();  // 0 = leader
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     // Prefix sum of the experts' token tiles: each thread sums up to three
     // consecutive experts, then warps, then the block.
     constexpr int PER = (kMaxExperts + THREADS - 1) / THREADS;
-    int* wsum = table + kMaxExperts + 1;
+    int* wsum = table + 2 * kMaxExperts + 1;
     const int e0 = threadIdx.x * PER;
     int c[PER], sum = 0;
     bool bad = false;
@@ -387,6 +392,8 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         const Span s = span_of(p, e0 + i);
         bad |= s.begin != __ldg(p.offsets + e0 + i) || s.end != __ldg(p.offsets + e0 + i + 1);
         c[i] = token_tiles<NT>(s.end - s.begin);
+        table[kMaxExperts + e0 + i] = s.begin;
+        if (e0 + i + 1 == p.experts) table[kMaxExperts + p.experts] = s.end;
       }
       sum += c[i];
     }
@@ -609,19 +616,22 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
             __syncwarp();
             // rows of 32 features: four lanes a row, 16 bytes a lane
             const int f = r0 + (lane & 3) * 8;
+            uint4 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int tk = 8 * j + (lane >> 2);
-              if (c + tk >= t.nvalid || f >= p.M) continue;
-              const uint4 v = *reinterpret_cast<const uint4*>(sd + sw64(tk, (lane & 3) * 8));
-              O* d = out + (long long)(t.n0 + c + tk) * p.ldo + f;
-              if (f + 8 <= p.M) {
-                *reinterpret_cast<uint4*>(d) = v;
-              } else {
-                const O* h = reinterpret_cast<const O*>(&v);
+            for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(sd + sw64(8 * j + (lane >> 2), (lane & 3) * 8));
+            O* d = out + (long long)(t.n0 + c + (lane >> 2)) * p.ldo + f;
+            const int left = t.nvalid - c - (lane >> 2);  // tokens from this lane's first row on
+            if (f + 8 <= p.M) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (8 * j < left) *reinterpret_cast<uint4*>(d + 8 * j * p.ldo) = v[j];
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const O* h = reinterpret_cast<const O*>(&v[j]);
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                  if (f + x < p.M) d[x] = h[x];
+                  if (8 * j < left && f + x < p.M) d[8 * j * p.ldo + x] = h[x];
               }
             }
           }
@@ -934,6 +944,8 @@ muon_status grouped_rows(const GroupedDesc& g, const void* x, const void* w, voi
   p.tokens = (int)g.tokens;
   p.experts = g.experts;
   p.a_mn = mn ? 1 : 0;
+  const unsigned mt = (unsigned)((p.M + grp::TILE_M - 1) / grp::TILE_M);
+  p.mt_inverse = (unsigned)((0x100000000ull + mt - 1) / mt);  // not used for mt = 1
   p.status = g.status;
   p.timeout_ns = timeout_ns;
   return g.type == Op::BF16 ? rows_typed<__nv_bfloat16>(p, nt, s) : rows_typed<__half>(p, nt, s);
