@@ -972,9 +972,9 @@ muon_status grouped_matmul_dw(const muon_grouped* g, const void* dy, const void*
   if (!dw || !g->offsets || (g->tokens > 0 && (!dy || !x))) return MUON_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(x) || !aligned16(dw) || (reinterpret_cast<uintptr_t>(g->offsets) & 3u))
     return MUON_ERR_ALIGN;
-  if (!ws || ws_bytes < grouped_ws(g->experts)) return MUON_ERR_WORKSPACE;
   const GroupedDesc d = grouped_desc(g, t);
   if (!grouped_fits(d)) return MUON_ERR_SHAPE;
+  if (!ws || ws_bytes < grouped_ws(g->experts)) return MUON_ERR_WORKSPACE;
   return grouped_dw(d, dy, x, dw, ot, alpha, beta, ws, timeout_ns(), static_cast<cudaStream_t>(stream));
 }
 

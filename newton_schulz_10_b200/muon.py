@@ -453,20 +453,28 @@ def _code_of(t, where: str) -> int:
     return code
 
 
+def _torch():
+    """torch and its 16-bit types, looked up once: the calls below are made for
+    a handful of tokens at a time, where every microsecond on the host counts."""
+    global _T
+    import torch
+    _T = (torch, torch.bfloat16, torch.float16, torch.int32, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    torch.cuda.init()  # _cuda_getDevice needs it
+    return _T
+
+
+_T = None
+
+
 def _call_on(device: int, stream, fn, args, where: str) -> None:
     """fn(*args, stream) with the CUDA device of the tensors current, on the
-    given stream or that device's current one. The raw stream handle and the
-    comparison with the current device keep this at about a microsecond,
-    which a call of a few tokens would notice."""
-    import torch
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-    if torch.cuda.current_device() == device:
+    given stream or that device's current one."""
+    t = _T or _torch()
+    raw = t[4](device) if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if t[5]() == device:
         code = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with t[0].cuda.device(device):
             code = fn(*args, raw)
     if code != OK:
         raise MuonError(code, where)
@@ -474,31 +482,38 @@ def _call_on(device: int, stream, fn, args, where: str) -> None:
 
 def _grouped(where, x, y, w, offsets, dev_status):
     """The descriptor and device of a call: x (tokens, k), y (tokens, n), w (experts, n, k)."""
-    import torch
-    xs, ys, ws, os_ = x.shape, y.shape, w.shape, offsets.shape
-    if len(xs) != 2 or len(ys) != 2 or len(ws) != 3 or len(os_) != 1:
-        raise MuonError(ERR_SHAPE, where)
-    tokens, k = xs
-    experts, n, wk = ws
-    if wk != k or ys[0] != tokens or ys[1] != n or os_[0] != experts + 1:
+    try:
+        (tokens, k), (yt, n), (experts, wn, wk), (entries,) = x.shape, y.shape, w.shape, offsets.shape
+    except ValueError:
+        raise MuonError(ERR_SHAPE, where) from None
+    if wk != k or wn != n or yt != tokens or entries != experts + 1:
         raise MuonError(ERR_SHAPE, where)
     dtype = x.dtype
-    if y.dtype != dtype or (dtype != torch.bfloat16 and dtype != torch.float16) or offsets.dtype != torch.int32:
-        raise MuonError(ERR_DTYPE, where)
     device = x.get_device()
+    if device < 0:  # before torch's CUDA side is needed
+        import torch
+        bf16, f16, i32 = torch.bfloat16, torch.float16, torch.int32
+    else:
+        bf16, f16, i32 = (_T or _torch())[1:4]
+    if y.dtype != dtype or (dtype != bf16 and dtype != f16) or offsets.dtype != i32:
+        raise MuonError(ERR_DTYPE, where)
     if device < 0 or y.get_device() != device or w.get_device() != device or offsets.get_device() != device:
         raise MuonError(ERR_INVALID_ARG, where)
-    xt, yt, wt = x.stride(), y.stride(), w.stride()
-    if (k > 1 and (xt[1] != 1 or wt[2] != 1)) or (n > 1 and yt[1] != 1) or (experts > 0 and offsets.stride(0) != 1):
+    (xr, xc), (yr, yc), (we, wr, wc) = x.stride(), y.stride(), w.stride()
+    if (k > 1 and (xc != 1 or wc != 1)) or (n > 1 and yc != 1) or (experts > 0 and offsets.stride(0) != 1):
         raise MuonError(ERR_SHAPE, where)
-    if dev_status is not None and (dev_status.dtype != torch.int32 or dev_status.get_device() != device):
-        raise MuonError(ERR_INVALID_ARG, where)
+    status = None
+    if dev_status is not None:
+        if dev_status.dtype != i32 or dev_status.get_device() != device:
+            raise MuonError(ERR_INVALID_ARG, where)
+        status = dev_status.data_ptr()
     # the stride of a single row is never used: any aligned value will do
-    kp, np_ = (k + 7) & ~7, (n + 7) & ~7
-    g = Grouped(BF16 if dtype == torch.bfloat16 else F16, experts, tokens, n, k, xt[0] if tokens > 1 else kp,
-                yt[0] if tokens > 1 else np_, wt[1] if n > 1 else kp, wt[0] if experts > 1 else 0, offsets.data_ptr(),
-                None if dev_status is None else dev_status.data_ptr())
-    return g, device
+    if tokens <= 1:
+        xr, yr = (k + 7) & ~7, (n + 7) & ~7
+    if n <= 1:
+        wr = (k + 7) & ~7
+    return Grouped(BF16 if dtype == bf16 else F16, experts, tokens, n, k, xr, yr, wr, we if experts > 1 else 0,
+                   offsets.data_ptr(), status), device
 
 
 def grouped_matmul(x, w, offsets, out=None, dev_status=None, stream=None):
@@ -508,28 +523,28 @@ def grouped_matmul(x, w, offsets, out=None, dev_status=None, stream=None):
     weights (bf16 or fp16, unit column stride, 16-byte rows), offsets
     (experts + 1, int32, on the device) each expert's first row. Rows of `out`
     (tokens, n) that belong to no expert keep their values."""
-    where = "grouped_matmul"
-    if x.dim() != 2 or w.dim() != 3:
-        raise MuonError(ERR_SHAPE, where)
+    if out is None:
+        _need(x.dim() == 2 and w.dim() == 3, ERR_SHAPE, "grouped_matmul")
+        out = x.new_empty((x.shape[0], w.shape[1]))
     if w.dtype != x.dtype:
-        raise MuonError(ERR_DTYPE, where)
-    y = x.new_empty((x.shape[0], w.shape[1])) if out is None else out
-    g, device = _grouped(where, x, y, w, offsets, dev_status)
-    _call_on(device, stream, lib().grouped_matmul, (C.byref(g), x.data_ptr(), w.data_ptr(), y.data_ptr()), where)
-    return y
+        raise MuonError(ERR_DTYPE, "grouped_matmul")
+    g, device = _grouped("grouped_matmul", x, out, w, offsets, dev_status)
+    _call_on(device, stream, (_lib or lib()).grouped_matmul, (C.byref(g), x.data_ptr(), w.data_ptr(), out.data_ptr()),
+             "grouped_matmul")
+    return out
 
 
 def grouped_matmul_dx(dy, w, offsets, out=None, dev_status=None, stream=None):
     """dx[r] = dy[r] @ w[e]: the gradient of grouped_matmul for its rows."""
-    where = "grouped_matmul_dx"
-    if dy.dim() != 2 or w.dim() != 3:
-        raise MuonError(ERR_SHAPE, where)
+    if out is None:
+        _need(dy.dim() == 2 and w.dim() == 3, ERR_SHAPE, "grouped_matmul_dx")
+        out = dy.new_empty((dy.shape[0], w.shape[2]))
     if w.dtype != dy.dtype:
-        raise MuonError(ERR_DTYPE, where)
-    dx = dy.new_empty((dy.shape[0], w.shape[2])) if out is None else out
-    g, device = _grouped(where, dx, dy, w, offsets, dev_status)
-    _call_on(device, stream, lib().grouped_matmul_dx, (C.byref(g), dy.data_ptr(), w.data_ptr(), dx.data_ptr()), where)
-    return dx
+        raise MuonError(ERR_DTYPE, "grouped_matmul_dx")
+    g, device = _grouped("grouped_matmul_dx", out, dy, w, offsets, dev_status)
+    _call_on(device, stream, (_lib or lib()).grouped_matmul_dx, (C.byref(g), dy.data_ptr(), w.data_ptr(), out.data_ptr()),
+             "grouped_matmul_dx")
+    return out
 
 
 def grouped_workspace_size(experts: int) -> int:
@@ -542,17 +557,18 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
     the type of dy and x. beta = 0 does not read `out`; without `out` the
     result is fp32. With beta = the momentum decay and an fp32 momentum as
     `out` this is M <- mu M + G without a gradient in memory."""
-    import torch
     where = "grouped_matmul_dw"
-    _need(dy.dim() == 2 and x.dim() == 2 and offsets.dim() == 1 and offsets.shape[0] >= 1, ERR_SHAPE, where)
+    _need(offsets.dim() == 1 and offsets.shape[0] >= 1, ERR_SHAPE, where)
     experts = offsets.shape[0] - 1
     if out is None:
+        import torch
+        _need(dy.dim() == 2 and x.dim() == 2, ERR_SHAPE, where)
         _need(beta == 0.0, ERR_INVALID_ARG, where)
         out = torch.empty((experts, dy.shape[1], -(-x.shape[1] // 8) * 8), dtype=torch.float32, device=x.device)[:, :, :x.shape[1]]
     g, device = _grouped(where, x, dy, out, offsets, dev_status)
     if ws is None:
         ws = workspace(grouped_workspace_size(experts), x.device)
-    _call_on(device, stream, lib().grouped_matmul_dw, (C.byref(g), dy.data_ptr(), x.data_ptr(), out.data_ptr(),
+    _call_on(device, stream, (_lib or lib()).grouped_matmul_dw, (C.byref(g), dy.data_ptr(), x.data_ptr(), out.data_ptr(),
                                                        _code_of(out, where), alpha, beta, ws.data_ptr(), ws.numel()), where)
     return out
 
