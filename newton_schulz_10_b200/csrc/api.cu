@@ -1128,7 +1128,9 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
   if (!aligned16(ws)) return MUON_ERR_ALIGN;
   if (ws_bytes < q.total) return MUON_ERR_WORKSPACE;
   int* status = p->dev_status ? p->dev_status : at<int>(ws, 0);
-  if (!p->dev_status && cudaMemsetAsync(status, 0, sizeof(int), s) != cudaSuccess) return MUON_ERR_CUDA;
+  // the momentum launch clears the status word where it comes first
+  const bool clear = !p->dev_status && q.small.empty() && q.groups.size() <= (size_t)kMaxStacks;
+  if (!p->dev_status && !clear && cudaMemsetAsync(status, 0, sizeof(int), s) != cudaSuccess) return MUON_ERR_CUDA;
 
   // bf16 operands are stored unscaled, in the momentum pass itself, and the
   // Frobenius scale enters the first products; the others are scaled once
@@ -1143,6 +1145,11 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
   proto.nesterov = p->nesterov;
   proto.folded = folded;
   proto.status = status;
+  proto.clear = clear;
+  // Up to 512 rows a warp adds the row sums (16 loads a lane) sooner than the
+  // next launch starts; the others' scale is also an operand of the products.
+  proto.sums = planes == 2;
+  for (const StackPlan::Grp& g : q.groups) proto.sums = proto.sums && st[g.stack].rows <= 512;
   auto add = [](StackLaunch& L, const muon_stack& k) -> StackMat& {
     StackMat& e = L.m[L.count++];
     e.W = k.W; e.w_stride = k.w_stride; e.w_ld = k.w_ld; e.w_type = k.w_dtype;
@@ -1203,7 +1210,7 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
   }
   for (StackLaunch& L : launches) {
     TRY(launch_stack_momentum(L, t, folded, s));
-    TRY(launch_stack_norm(L, s));
+    if (!L.sums) TRY(launch_stack_norm(L, s));
     if (!folded) TRY(launch_stack_cast(L, t, planes, s));
   }
   for (size_t g0 = 0; g0 < groups.size(); g0 += kMaxGemmGroups) {

@@ -45,6 +45,8 @@ __global__ void __launch_bounds__(BLOCK) stack_momentum(const __grid_constant__ 
   __shared__ double scratch[32];
   grid_dependency_wait();
   grid_dependents_launch();
+  // the launches that may report come after this one
+  if (L.clear && blockIdx.x == 0 && threadIdx.x == 0) *L.status = MUON_OK;
   const int task = blockIdx.x * (BLOCK / WG) + threadIdx.x / WG;
   const int l = threadIdx.x % WG;
   const bool active = task < L.total_rows;
@@ -103,8 +105,21 @@ __global__ void __launch_bounds__(BLOCK) stack_momentum(const __grid_constant__ 
   if (active && l == 0) L.rsum[task] = ss;
 }
 
-// One warp per matrix. A matrix of zeros gets scale 0 (its update is 0, also
-// with eps = 0); the scale of a norm below 1 / FLT_MAX is FLT_MAX.
+// 1 / (norm + eps) from the sum of squares. A matrix of zeros gets scale 0
+// (its update is 0, also with eps = 0); the scale of a norm below 1 / FLT_MAX
+// is FLT_MAX.
+__device__ __forceinline__ float scale_of(double t, float eps) {
+  const double inv = t > 0.0 ? 1.0 / (sqrt(t) + (double)eps) : 0.0;
+  return inv > 3.4028234663852886e38 ? 3.4028234663852886e38f : (float)inv;
+}
+// Sum of a matrix's row sums by a warp, in a fixed order.
+__device__ __forceinline__ double sum_rows(const double* r, int rows, int lane) {
+  double t = 0.0;
+  for (int k = lane; k < rows; k += 32) t += r[k];
+  return warp_sum(t);
+}
+
+// One warp per matrix.
 __global__ void __launch_bounds__(BLOCK) stack_norm(const __grid_constant__ StackLaunch L) {
   grid_dependency_wait();
   grid_dependents_launch();
@@ -116,14 +131,10 @@ __global__ void __launch_bounds__(BLOCK) stack_norm(const __grid_constant__ Stac
     if (L.m[mid].mat_begin <= i) lo = mid; else hi = mid - 1;
   }
   const StackMat& m = L.m[lo];
-  const double* r = L.rsum + m.row_begin + (int64_t)(i - m.mat_begin) * m.rows;
-  double t = 0.0;
-  for (int k = lane; k < m.rows; k += 32) t += r[k];
-  t = warp_sum(t);
+  const double t = sum_rows(L.rsum + m.row_begin + (int64_t)(i - m.mat_begin) * m.rows, m.rows, lane);
   if (lane == 0) {
     if (!isfinite(t)) report(L.status, MUON_ERR_NONFINITE);
-    const double inv = t > 0.0 ? 1.0 / (sqrt(t) + (double)L.eps) : 0.0;
-    const float s = inv > 3.4028234663852886e38 ? 3.4028234663852886e38f : (float)inv;
+    const float s = scale_of(t, L.eps);
     L.scale[i] = s;
     L.xscale[i] = L.folded ? s : 1.f / m.kappa;
   }
@@ -131,7 +142,8 @@ __global__ void __launch_bounds__(BLOCK) stack_norm(const __grid_constant__ Stac
 
 // X <- scale * target * kappa: the gradient is read again for Nesterov's
 // target (2 or 4 bytes an element against 8 for writing the target in fp32
-// and reading it back).
+// and reading it back). With L.sums each warp adds its matrix's row sums
+// itself: where there are few rows (stack_impl) that is less than a launch.
 template <int WG, typename T, int PL>
 __global__ void __launch_bounds__(BLOCK) stack_cast(const __grid_constant__ StackLaunch L) {
   grid_dependency_wait();
@@ -145,7 +157,15 @@ __global__ void __launch_bounds__(BLOCK) stack_cast(const __grid_constant__ Stac
   const void* G = m.G && L.nesterov ? row_at(m.G, m.g_type, w.b * m.g_stride + w.r * m.g_ld) : nullptr;
   T* X = static_cast<T*>(m.X) + ((int64_t)w.b * PL * m.rows + w.r) * m.ldx;
   T* Y = X + (int64_t)m.rows * m.ldx;  // the low plane
-  const float sc = L.scale[m.mat_begin + w.b], kappa = m.kappa, mu = L.mu;
+  float sc;
+  if (L.sums) {
+    const double t = sum_rows(L.rsum + m.row_begin + (int64_t)w.b * m.rows, m.rows, threadIdx.x & 31);
+    if (!isfinite(t) && w.r == 0 && l == 0) report(L.status, MUON_ERR_NONFINITE);
+    sc = scale_of(t, L.eps);
+  } else {
+    sc = L.scale[m.mat_begin + w.b];
+  }
+  const float kappa = m.kappa, mu = L.mu;
   if (m.vec) {
     const int n4 = m.cols >> 2;
 #pragma unroll UNROLL

@@ -36,6 +36,8 @@ struct StackLaunch {
   float eps;
   int nesterov;
   int folded;     // the operand is stored unscaled, scale enters the first products
+  int sums;       // the cast adds the row sums itself (no launch_stack_norm)
+  int clear;      // the momentum launch sets *status to MUON_OK
   int* status;
 };
 static_assert(sizeof(StackLaunch) <= 32764, "kernel parameters are limited to 32764 bytes");
