@@ -446,7 +446,9 @@ typedef struct {
  *   nesterov      1: orthogonalise G + mu M (M already updated) instead of M;
  *                 needs G
  *   ns            compute may be MUON_F16X2 (gram = 0 only, else
- *                 MUON_ERR_UNSUPPORTED)
+ *                 MUON_ERR_UNSUPPORTED). Its operands, and fp16's, are scaled
+ *                 for coefficients up to 15 in magnitude; a polynomial that
+ *                 leaves fp16's range is reported as MUON_ERR_NONFINITE
  *   dev_status    as in muon_params */
 typedef struct {
   float mu;

@@ -104,6 +104,16 @@ T* at(void* ws, size_t off) {
     if (_r != MUON_OK) return _r;     \
   } while (0)
 
+// Runs f; an exception (no host memory for a table) becomes a status.
+template <typename F>
+muon_status guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return MUON_ERR_CUDA;
+  }
+}
+
 // Launch a row kernel over any number of matrices, kMaxRowMats at a time.
 template <typename F>
 muon_status row_batches(const std::vector<RowMat>& mats, const RowLaunch& proto, F launch) {
@@ -915,7 +925,7 @@ muon_status muon_apply_update(const muon_matrix* mats, int32_t count, const muon
 namespace {
 
 // Shapes, strides and types of a grouped call; pointers are checked by each
-// entry point. out_bytes: element size of the weights' side (dW may be fp32).
+// entry point. w_bytes: element size of the weights' side (dW may be fp32).
 muon_status check_grouped(const muon_grouped* g, int w_bytes, Op* t) {
   if (!g) return MUON_ERR_INVALID_ARG;
   if (g->dtype != MUON_BF16 && g->dtype != MUON_F16) return MUON_ERR_DTYPE;
@@ -951,11 +961,11 @@ muon_status grouped_rows_impl(const muon_grouped* g, const void* x, const void* 
 }  // namespace
 
 muon_status grouped_matmul(const muon_grouped* g, const void* x, const void* w, void* y, void* stream) {
-  return grouped_rows_impl(g, x, w, y, false, stream);
+  return guarded([&] { return grouped_rows_impl(g, x, w, y, false, stream); });
 }
 
 muon_status grouped_matmul_dx(const muon_grouped* g, const void* dy, const void* w, void* dx, void* stream) {
-  return grouped_rows_impl(g, dy, w, dx, true, stream);
+  return guarded([&] { return grouped_rows_impl(g, dy, w, dx, true, stream); });
 }
 
 size_t grouped_workspace_size(int32_t experts) {
@@ -975,7 +985,7 @@ muon_status grouped_matmul_dw(const muon_grouped* g, const void* dy, const void*
   const GroupedDesc d = grouped_desc(g, t);
   if (!grouped_fits(d)) return MUON_ERR_SHAPE;
   if (!ws || ws_bytes < grouped_ws(g->experts)) return MUON_ERR_WORKSPACE;
-  return grouped_dw(d, dy, x, dw, ot, alpha, beta, ws, timeout_ns(), static_cast<cudaStream_t>(stream));
+  return guarded([&] { return grouped_dw(d, dy, x, dw, ot, alpha, beta, ws, timeout_ns(), static_cast<cudaStream_t>(stream)); });
 }
 
 // ---------------------------------------------------------------------------
@@ -1234,17 +1244,22 @@ void muon_stack_params_default(muon_stack_params* p) {
 }
 
 size_t muon_stack_workspace_size(const muon_stack* stacks, int32_t count, const muon_stack_params* p) {
-  Op t;
-  int planes;
-  if (check_stacks(stacks, count, p, true, &t, &planes) != MUON_OK) return 0;
-  muon_ns_params ns = p->ns;
-  if (planes == 2) ns.compute = MUON_F16;
-  return plan_stacks(stacks, count, &ns, t, planes).total;
+  size_t bytes = 0;
+  guarded([&] {
+    Op t;
+    int planes;
+    TRY(check_stacks(stacks, count, p, true, &t, &planes));
+    muon_ns_params ns = p->ns;
+    if (planes == 2) ns.compute = MUON_F16;
+    bytes = plan_stacks(stacks, count, &ns, t, planes).total;
+    return MUON_OK;
+  });
+  return bytes;
 }
 
 muon_status muon_stack_step(const muon_stack* stacks, int32_t count, const muon_stack_params* p, void* ws, size_t ws_bytes,
                             void* stream) {
-  return stack_impl(stacks, count, p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+  return guarded([&] { return stack_impl(stacks, count, p, ws, ws_bytes, static_cast<cudaStream_t>(stream)); });
 }
 
 int64_t muon_kernel_launch_count(void) { return counters().launches; }

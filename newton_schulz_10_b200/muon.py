@@ -437,7 +437,8 @@ def muon_step(mats, p: Params | None = None, ws=None, stream=None) -> Step:
 
 
 # ---------------------------------------------------------------------------
-# products grouped by expert
+# products grouped by expert (explicit forward and gradient calls, as in the
+# rest of this binding: nothing here is recorded by autograd)
 # ---------------------------------------------------------------------------
 
 
@@ -551,6 +552,20 @@ def grouped_workspace_size(experts: int) -> int:
     return lib().grouped_workspace_size(experts)
 
 
+def _workspace_on(stream, experts: int, device):
+    """A workspace of grouped_matmul_dw from the memory pool of the stream that
+    uses it (the caching allocator hands a freed block out again in the order
+    of the stream it was allocated on)."""
+    import torch
+    with torch.cuda.device(device):
+        n = grouped_workspace_size(experts)
+        if stream is None:
+            return workspace(n, device)
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device)
+        with torch.cuda.stream(s):
+            return workspace(n, device)
+
+
 def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float = 0.0, ws=None, dev_status=None, stream=None):
     """out[e] = alpha * dy_e.T @ x_e + beta * out[e] over the rows of expert e:
     the gradient of grouped_matmul for its weights (experts, n, k), in fp32 or
@@ -567,7 +582,7 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
         out = torch.empty((experts, dy.shape[1], -(-x.shape[1] // 8) * 8), dtype=torch.float32, device=x.device)[:, :, :x.shape[1]]
     g, device = _grouped(where, x, dy, out, offsets, dev_status)
     if ws is None:
-        ws = workspace(grouped_workspace_size(experts), x.device)
+        ws = _workspace_on(stream, experts, x.device)
     _call_on(device, stream, (_lib or lib()).grouped_matmul_dw, (C.byref(g), dy.data_ptr(), x.data_ptr(), out.data_ptr(),
                                                        _code_of(out, where), alpha, beta, ws.data_ptr(), ws.numel()), where)
     return out
@@ -670,7 +685,7 @@ class StackStep:
         k = self.stacks[i]
         _need(k.G is None, ERR_INVALID_ARG, "StackStep.accumulate")
         if self._grouped_ws[i] is None:
-            self._grouped_ws[i] = workspace(grouped_workspace_size(k.M.shape[0]), k.M.device)
+            self._grouped_ws[i] = _workspace_on(stream, k.M.shape[0], k.M.device)
         grouped_matmul_dw(dy, x, offsets, out=k.M, beta=self.params.mu, ws=self._grouped_ws[i], stream=stream)
 
     def device_status(self) -> int:

@@ -337,3 +337,62 @@ def test_short_device_wait_is_reported(cuda, rows):
         assert int(status.item()) == mu.OK
     for r, want, mag in rows_ref(x, w, off, True):
         close(mu.grouped_matmul(x, w, off)[r], want, mag, 8192, d)
+
+
+def test_weight_gradient_on_another_stream_without_a_workspace(cuda):
+    """The workspace that the call makes for itself belongs to the stream that uses it."""
+    d = torch.bfloat16
+    x, dy, off = draw((5000, 256), 1.0, d, 1), draw((5000, 256), 1.0, d, 2), offsets_of([3000, 2000])
+    want = mu.grouped_matmul_dw(dy, x, off)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(8):
+        out = torch.zeros((2, 256, 256), device="cuda")
+        s.wait_stream(torch.cuda.current_stream())
+        mu.grouped_matmul_dw(dy, x, off, out=out, stream=s)
+        torch.full((6_000_000,), float("nan"), device="cuda")  # would land in a workspace freed on this stream
+        got.append(out)
+    raw = torch.zeros((2, 256, 256), device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    mu.grouped_matmul_dw(dy, x, off, out=raw, stream=s.cuda_stream)
+    s.synchronize()
+    assert all(torch.equal(g, want) for g in got) and torch.equal(raw, want)
+
+
+@pytest.mark.parametrize("counts", [[2000, 1000, 0, 500], [0, 0, 3500, 0]])
+def test_graph_replay_of_cut_sums(cuda, counts):
+    """Few tiles over many rows: the sums are cut into parts; a captured call follows the offsets it finds."""
+    d = torch.float16
+    x, dy = draw((3500, 72), 1.0, d, 1), draw((3500, 136), 1.0, d, 2)
+    off = offsets_of([875, 875, 875, 875])
+    dw, ws = draw((4, 136, 72), 1.0, torch.float32, 3), mu.workspace(mu.grouped_workspace_size(4))
+    old = dw.clone()
+    mu.grouped_matmul_dw(dy, x, off, out=dw, beta=0.5, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mu.grouped_matmul_dw(dy, x, off, out=dw, beta=0.5, ws=ws)
+    off.copy_(offsets_of(counts))
+    dw.copy_(old)
+    graph.replay()
+    torch.cuda.synchronize()
+    want, mag = dw_ref(dy, x, off, 1.0, 0.5, old)
+    assert bool(((dw.double() - want).abs() <= 2.0 ** -22 * (want.abs() + old.double().abs()) + (max(counts) / 16 + 8) * 2.0 ** -23 * mag).all())
+
+
+def test_two_calls_at_once(cuda):
+    """Two streams, each with its own outputs and workspace, on the same inputs."""
+    d = torch.bfloat16
+    x, dy, w = draw((3000, 512), 1.0, d, 1), draw((3000, 384), 1.0, d, 2), draw((5, 384, 512), 0.05, d, 3)
+    off = offsets_of([700, 0, 1500, 300, 500])
+    want = (mu.grouped_matmul(x, w, off), mu.grouped_matmul_dx(dy, w, off), mu.grouped_matmul_dw(dy, x, off))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append((mu.grouped_matmul(x, w, off), mu.grouped_matmul_dx(dy, w, off), mu.grouped_matmul_dw(dy, x, off)))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))

@@ -337,3 +337,39 @@ def test_on_another_stream(cuda):
         step()
     s.synchronize()
     assert torch.equal(W1, W2) and torch.equal(M1, M2)
+
+
+def test_two_updates_at_once(cuda):
+    """Two streams, each with its own tensors and workspace: small matrices on chip and larger ones by the chain."""
+    p = mu.stack_params(nesterov=True, weight_decay=0.1, ns=mu.ns_params(compute=mu.F16X2))
+    shapes = [(6, 64, 200), (2, 200, 330)]
+
+    def make():
+        return [mu.Stack(gauss(s, 101, 0.02), gauss(s, 102), gauss(s, 103)) for s in shapes]
+
+    ref = make()
+    for _ in range(3):
+        mu.stack_step(ref, p)
+    sets = [make() for _ in range(2)]
+    steps = [mu.StackStep(s, p) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for s, step in zip(streams, steps):
+            step(stream=s)
+    torch.cuda.synchronize()
+    for stacks in sets:
+        for a, b in zip(stacks, ref):
+            assert torch.equal(a.W, b.W) and torch.equal(a.M, b.M)
+
+
+def test_accumulate_needs_no_gradient_and_nesterov_needs_one(cuda):
+    W, M, G = gauss((2, 16, 24), 1), gauss((2, 16, 24), 2), gauss((2, 16, 24), 3)
+    off = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    dy, x = gauss((5, 16), 4, dtype=torch.bfloat16), gauss((5, 24), 5, dtype=torch.bfloat16)
+    with pytest.raises(mu.MuonError) as err:
+        mu.StackStep([mu.Stack(W, M, G)], mu.stack_params()).accumulate(0, dy, x, off)
+    assert err.value.code == mu.ERR_INVALID_ARG
+    with pytest.raises(mu.MuonError) as err:
+        mu.StackStep([mu.Stack(W, M)], mu.stack_params(nesterov=True))()
+    assert err.value.code == mu.ERR_INVALID_ARG
