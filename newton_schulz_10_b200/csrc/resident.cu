@@ -7,7 +7,7 @@
 // few microseconds each, every one paying a launch, its setup, a pipeline
 // fill and a drain. Here a cluster of C CTAs (1 to 16) holds one matrix:
 // CTA r keeps columns [r mc, (r+1) mc) of the wide view X (n x m) in shared
-// memory, mc = 64 g <= 256, as operands of tcgen05.mma; per step
+// memory, mc = 64 g <= 512, as operands of tcgen05.mma; per step
 //   A  = sum over the cluster of X_r X_r^T   (M = 128, N = n, K = mc)
 //   B' = a I + b A + c A A                   (every CTA, K = n)
 //   X_r <- B' X_r                            (N = mc, K = n)
@@ -54,24 +54,24 @@ constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_N = 128;      // rows of the wide view
 constexpr int MAX_M = 2048;     // columns of the wide view
-constexpr int MAX_G = 4;        // 64-column groups per CTA
+constexpr int MAX_G = 8;        // 64-column groups per CTA (their accumulators fill TMEM)
 constexpr int MAX_C = 16;       // CTAs per cluster (above 8 only where a smaller one cannot hold the matrix)
-constexpr int GROUP = 128 * 128;  // bytes of one 64-column group of one plane
 constexpr int MISC = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr uint64_t DRAIN_NS = 1000000000ull;
-constexpr int X_COL = 128;      // TMEM column of X's accumulator (A's is 0)
-
 constexpr int SMEM_MAX = 232448;  // opt-in shared memory of one sm_100 CTA
 
+// A 64-column group of a plane: np rows of 128 bytes.
+constexpr int group_bytes(int np) { return np * 128; }
 // X (g groups) and A (np rows and columns), two planes each, and with a
-// cluster the np x np fp32 sums. At least 120 KB, so that an SM holds one CTA
-// (two would wait for each other's TMEM columns).
+// cluster the np x np fp32 sums; the M side of a product reads 128 rows from
+// a group's start, so as much must lie behind the last one. At least 120 KB,
+// so that an SM holds one CTA (two would wait for each other's TMEM columns).
 constexpr int smem_bytes(int g, int np, int C) {
-  const int b = 1024 + 2 * g * GROUP + 2 * ((np + 63) / 64) * GROUP + (C > 1 ? np * np * 4 : 0) + MISC;
+  const int b = 1024 + 2 * (g + (np + 63) / 64) * group_bytes(np) + (C > 1 ? np * np * 4 : 0) + MISC + group_bytes(128 - np);
   return b > 120 * 1024 ? b : 120 * 1024;
 }
-static_assert(smem_bytes(MAX_G, MAX_N, 1) <= SMEM_MAX && smem_bytes(2, MAX_N, MAX_C) <= SMEM_MAX, "every shape fits");
+static_assert(smem_bytes(4, MAX_N, 1) <= SMEM_MAX && smem_bytes(2, MAX_N, MAX_C) <= SMEM_MAX, "every shape fits");
 
 struct Params {
   StackMat m;
@@ -190,11 +190,11 @@ template <typename T, int PL>
 __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int g = p.g, C = p.C;
+  const int g = p.g, C = p.C, group = group_bytes(p.np);
   uint8_t* const X = smem;                     // high plane: g groups; low plane behind
-  uint8_t* const Xl = X + g * GROUP;
-  uint8_t* const A = X + 2 * g * GROUP;        // high plane; low plane behind
-  const int a_plane = (p.np + 63) / 64 * GROUP;
+  uint8_t* const Xl = X + g * group;
+  uint8_t* const A = X + 2 * g * group;        // high plane; low plane behind
+  const int a_plane = (p.np + 63) / 64 * group;
   uint8_t* const Al = A + a_plane;
   uint8_t* const R = Al + a_plane;  // cluster: partial sums of this CTA's rows, [C][np / C][np] fp32
   double* slots = reinterpret_cast<double*>(R + (C > 1 ? p.np * p.np * 4 : 0));  // one partial norm per CTA of the cluster
@@ -223,11 +223,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
-  // rows 0..np of every group: zeros where the matrix has no element
-  for (int i = tid; i < 2 * g * p.np * 8; i += THREADS) {
-    const int grp = i / (p.np * 8), rest = i - grp * p.np * 8;
-    *reinterpret_cast<uint4*>(X + grp * GROUP + rest * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
+  // zeros where the matrix has no element
+  for (int i = tid; i < 2 * g * group / 16; i += THREADS) reinterpret_cast<uint4*>(X)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc_fence_before();
   sync_all();  // also: every CTA of the cluster has started, so its shared memory may be written
   tc_fence_after();
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   // byte offset (within a plane) of stored element (r, c) of this CTA
   auto spot = [&](int r, int c) -> uint32_t {
     const int i = p.tall ? c : r, j = p.tall ? r : c;
-    return (uint32_t)((j >> 6) * GROUP) + at(i, (j & 63) >> 3) + (j & 7) * 2;
+    return (uint32_t)((j >> 6) * group) + at(i, (j & 63) >> 3) + (j & 7) * 2;
   };
   auto put_raw = [&](int r, int c, float v) {
     const uint32_t o = spot(r, c), u = __float_as_uint(v);
@@ -332,14 +329,13 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   const double inv = total > 0.0 ? 1.0 / (sqrt(total) + (double)p.eps) : 0.0;
   const float sc = inv > 3.4028234663852886e38 ? 3.4028234663852886e38f : (float)inv;
   __syncthreads();  // every element is in place
-  for (int i = tid; i < g * p.np * 8; i += THREADS) {
-    const int grp = i / (p.np * 8), rest = i - grp * p.np * 8;
-    uint8_t* h = X + grp * GROUP + rest * 16;
+  for (int i = tid; i < g * group / 16; i += THREADS) {
+    uint8_t* h = X + i * 16;
     float v[8];
-    get8_raw(h, h + g * GROUP, v);
+    get8_raw(h, h + g * group, v);
 #pragma unroll
     for (int x = 0; x < 8; ++x) v[x] = v[x] * sc * p.kappa;
-    put8<T, PL>(h, h + g * GROUP, v);
+    put8<T, PL>(h, h + g * group, v);
   }
 
   // ------------------------------------------------------------------
@@ -350,10 +346,11 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
   // shared-memory window carry the CTA's rank and must not reach the other fields.
   const uint32_t a_a = smem_u32(A);
   const uint32_t x_d = smem_u32(X) & 0x3FFFFu, a_d = a_a & 0x3FFFFu;
-  const uint32_t x_low = PL == 2 ? (uint32_t)(g * GROUP) >> 4 : 0u, a_low = (uint32_t)a_plane >> 4;
+  const uint32_t x_low = PL == 2 ? (uint32_t)(g * group) >> 4 : 0u, a_low = (uint32_t)a_plane >> 4;
   const uint64_t k_major = smem_desc_sw128(0, 16, 1024);       // 8-row groups 1 KB apart
-  const uint64_t mn_major = smem_desc_sw128(0, GROUP, 1024);   // 64-column atoms 16 KB apart
-  const uint32_t idesc_n = idesc_f16(fmt, 0, 0, 128, p.np), idesc_x = idesc_f16(fmt, 0, 1, 128, mc);
+  const uint64_t mn_major = smem_desc_sw128(0, group, 1024);   // 64-column atoms a group apart
+  const uint32_t idesc_n = idesc_f16(fmt, 0, 0, 128, p.np), idesc_x = idesc_f16(fmt, 0, 1, 128, min(mc, 256)),
+                 idesc_x2 = idesc_f16(fmt, 0, 1, 128, mc > 256 ? mc - 256 : 64);  // N is at most 256
   uint32_t parity = 0;
   // after the operands are written: order them before the products, which
   // warp 0 issues, and wait for their completion. A wait that runs out
@@ -412,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       for (int j = 0; j < g; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint64_t d = k_major | (uint64_t)((x_d + j * GROUP + k * 32) >> 4);
+          const uint64_t d = k_major | (uint64_t)((x_d + j * group + k * 32) >> 4);
           mma(on, tmem, d, d, x_low, x_low, idesc_n, j != 0 || k != 0);
         }
     });
@@ -423,8 +420,9 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       for (int k = 0; k < 4; ++k) {
         if (k >= chunks) break;
         const int c0 = half * 16 + 32 * k;
+        if (row >= p.np) continue;
         if (C == 1) {
-          const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
+          const uint32_t o = (uint32_t)((c0 >> 6) * group);
 #pragma unroll
           for (int x = 0; x < 16; ++x) v[k][x] *= alpha;
 #pragma unroll
@@ -432,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
             const uint32_t w = o + at(row, ((c0 & 63) >> 3) + s);
             put8<T, 2>(A + w, Al + w, v[k] + 8 * s);
           }
-        } else if (row < p.np) {
+        } else {
           // partial sums in fp32 where A's planes go: B' of the last step has
           // been read, and the peers send rows of A only once this CTA's
           // partial sums have left
@@ -451,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       if (warp == 0) {
         if (lane == 0) {
           mbar_arrive_expect_tx(sums, part * C);
-          mbar_arrive_expect_tx(rows, (uint32_t)(2 * a_plane / GROUP * p.np * 128));
+          mbar_arrive_expect_tx(rows, (uint32_t)(2 * a_plane));
         }
         __syncwarp();
         if (lane < C) {
@@ -484,17 +482,17 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
         }
 #pragma unroll
         for (int x = 0; x < 8; ++x) v[x] *= alpha;
-        const uint32_t w = (uint32_t)((c0 >> 6) * GROUP) + at(rank * rows_per + lr, (c0 & 63) >> 3);
+        const uint32_t w = (uint32_t)((c0 >> 6) * group) + at(rank * rows_per + lr, (c0 & 63) >> 3);
         put8<T, 2>(A + w, Al + w, v);
       }
       fence_operands();
       __syncthreads();
       // and to the peers: every CTA's partial sums have left its A
-      const int pieces = 2 * a_plane / GROUP;  // groups of both planes, contiguous
+      const int pieces = 2 * a_plane / group;  // groups of both planes, contiguous
       for (int i = tid; i < pieces * C; i += THREADS) {
         const int to = i / pieces;
         if (to == rank) continue;
-        const uint32_t o = a_a + (i - to * pieces) * GROUP + rank * rows_per * 128;
+        const uint32_t o = a_a + (i - to * pieces) * group + rank * rows_per * 128;
         copy_cluster(mapa_shared(o, (uint32_t)to), o, (uint32_t)(rows_per * 128), mapa_shared(smem_u32(rows), (uint32_t)to));
       }
       if (tid == 0) mbar_complete_tx(rows, (uint32_t)(pieces * rows_per * 128));  // its own are there
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     // B' = a I + b A + c A A, in A's place (every thread rewrites what it read)
     products([&](uint32_t on) {
       for (int k = 0; k < p.np / 16; ++k) {
-        const uint64_t d = k_major | (uint64_t)((a_d + (k >> 2) * GROUP + (k & 3) * 32) >> 4);
+        const uint64_t d = k_major | (uint64_t)((a_d + (k >> 2) * group + (k & 3) * 32) >> 4);
         mma(on, tmem, d, d, a_low, a_low, idesc_n, k != 0);
       }
     });
@@ -512,9 +510,9 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       const int chunks = load_chunks(y);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (k >= chunks) break;
+        if (k >= chunks || row >= p.np) break;
         const int c0 = half * 16 + 32 * k;
-        const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
+        const uint32_t o = (uint32_t)((c0 >> 6) * group);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const uint32_t w = o + at(row, ((c0 & 63) >> 3) + s);
@@ -532,9 +530,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     // X <- B' X
     products([&](uint32_t on) {
       for (int k = 0; k < p.np / 16; ++k) {
-        const uint64_t ad = k_major | (uint64_t)((a_d + (k >> 2) * GROUP + (k & 3) * 32) >> 4);
+        const uint64_t ad = k_major | (uint64_t)((a_d + (k >> 2) * group + (k & 3) * 32) >> 4);
         const uint64_t bd = mn_major | (uint64_t)((x_d + k * 2048) >> 4);
-        mma(on, tmem + X_COL, ad, bd, a_low, x_low, idesc_x, k != 0);
+        mma(on, tmem, ad, bd, a_low, x_low, idesc_x, k != 0);
+        if (mc > 256) mma(on, tmem + 256, ad, bd + (uint32_t)(4 * group >> 4), a_low, x_low, idesc_x2, k != 0);
       }
     });
     const bool last = t + 1 == p.T;
@@ -542,10 +541,10 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     if (rows_here)
       for (int c0 = half * 32; c0 < mc; c0 += 64) {  // one group an iteration
         uint32_t r[32];
-        tmem_ld_32x32(tl + X_COL + c0, r);
+        tmem_ld_32x32(tl + c0, r);
         tmem_wait_ld();
         if (row < p.np) {
-          const uint32_t o = (uint32_t)((c0 >> 6) * GROUP);
+          const uint32_t o = (uint32_t)((c0 >> 6) * group);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             float v[8];
@@ -726,7 +725,7 @@ bool resident_fits(int64_t rows, int64_t cols, int64_t count, int T, int planes,
     const int g = (groups + C - 1) / C;
     if (g > res::MAX_G || res::smem_bytes(g, np, C) > res::SMEM_MAX) continue;
     if (C > 8 && best_C) break;  // only where a smaller cluster cannot hold the matrix
-    const double step = 2000.0 + 900.0 * g + 14.0 * np + std::max(14.0 * np, 6.6 * np * g) + 700.0 * g + 19.0 * np +
+    const double step = 2000.0 + 900.0 * g + 14.0 * np + std::max(14.0 * np * ((g + 3) / 4), 6.6 * np * g) + 700.0 * g + 19.0 * np +
                         (C > 1 ? 1700.0 + 0.55 * np * np : 1000.0);
     const double waves = (double)((count + cluster_capacity(C) - 1) / cluster_capacity(C));
     const double t = waves * (12000.0 + 0.4 * n * 64 * g + T * step);
