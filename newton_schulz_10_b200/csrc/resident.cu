@@ -304,18 +304,32 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       }
     }
   } else {
-    for (int r = warp; r < srows; r += WARPS)
+    constexpr int U = 8;
+    for (int r0 = warp; r0 < srows; r0 += WARPS * U)
       for (int c = lane; c < scols; c += 32) {
-        float* q = M + (srow0 + r) * m.m_ld + scol0 + c;
-        float v = *q;
-        if (G) {
-          const float gr = load1(row_at(G, m.g_type, (srow0 + r) * m.g_ld + scol0), m.g_type, c);
-          v = fmaf(p.mu, v, gr);
-          *q = v;
-          v = target(v, gr, p.mu, p.nesterov);
+        float y[U], gr[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r < srows) {
+            y[u] = M[(srow0 + r) * m.m_ld + scol0 + c];
+            if (G) gr[u] = load1(row_at(G, m.g_type, (srow0 + r) * m.g_ld + scol0), m.g_type, c);
+            if (lane % 8 == 0) prefetch_l2(row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0 + c));
+          }
         }
-        put_raw(r, c, v);
-        ss += (double)v * (double)v;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r >= srows) break;
+          float v = y[u];
+          if (G) {
+            v = fmaf(p.mu, v, gr[u]);
+            M[(srow0 + r) * m.m_ld + scol0 + c] = v;
+            v = target(v, gr[u], p.mu, p.nesterov);
+          }
+          put_raw(r, c, v);
+          ss += (double)v * (double)v;
+        }
       }
   }
   double total = block_sum(ss, scratch);
@@ -597,14 +611,25 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
       }
     }
   } else {
-    for (int r = warp; r < srows; r += WARPS)
+    constexpr int U = 8;
+    for (int r0 = warp; r0 < srows; r0 += WARPS * U)
       for (int c = lane; c < scols; c += 32) {
-        const float o = get_raw(r, c);
-        bad |= !isfinite(o);
-        void* wr = row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0);
-        const float v = fmaf(-p.step, o, p.keep * load1(wr, m.w_type, c));
-        store1(wr, m.w_type, c, v);
-        if (K) store1(row_at(K, m.c_type, (srow0 + r) * m.c_ld + scol0), m.c_type, c, v);
+        float w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r < srows) w[u] = load1(row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0), m.w_type, c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = r0 + u * WARPS;
+          if (r >= srows) break;
+          const float o = get_raw(r, c);
+          bad |= !isfinite(o);
+          const float v = fmaf(-p.step, o, p.keep * w[u]);
+          store1(row_at(W, m.w_type, (srow0 + r) * m.w_ld + scol0), m.w_type, c, v);
+          if (K) store1(row_at(K, m.c_type, (srow0 + r) * m.c_ld + scol0), m.c_type, c, v);
+        }
       }
   }
   if (bad) report(p.status, MUON_ERR_NONFINITE);
