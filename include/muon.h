@@ -55,8 +55,10 @@ typedef enum {
 
 /* MUON_F16X2 is no element type of memory: as muon_ns_params.compute of
  * muon_stack_step it keeps every operand of the chain as the sum of two fp16
- * planes (22 bits), about fp32 accuracy on the tensor cores. The other entry
- * points answer it with MUON_ERR_DTYPE. */
+ * planes (22 bits) on the tensor cores. O is then off by about 1e-5 (Frobenius,
+ * relative) up to n = 256, 4e-5 at 1024 x 1024 and 1e-4 at 4096 x 4096, where
+ * MUON_F32 stays at 6e-6. The other entry points answer it with
+ * MUON_ERR_DTYPE. */
 typedef enum { MUON_F32 = 0, MUON_BF16 = 1, MUON_F16 = 2, MUON_F16X2 = 3 } muon_dtype;
 
 /* Dion3 row-selection key: the page's rule is the l1 norm of each momentum

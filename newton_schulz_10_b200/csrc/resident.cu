@@ -732,14 +732,14 @@ int cluster_capacity(int C) {
 // products takes at least 75 cycles, an epilogue 700 a group of X and 75 per
 // four rows and columns of B', the exchange 1700 + 0.55 np^2 whatever C is,
 // loads and stores 0.4 an element. Larger clusters halve the work on X and
-// pay the exchange: 12 x 64 x 768 takes 46 us on 8 CTAs a matrix and 52 on 4,
-// 1 x 128 x 128 takes 69 on 2 and 49 on 1, 16 x 128 x 512 (two waves of
-// clusters of 8) 146 on 8 and 76 on 2.
+// pay the exchange: 12 x 64 x 768 takes 45 us on 8 CTAs a matrix and 51 on 4,
+// 1 x 128 x 128 takes 68 on 2 and 47 on 1, 16 x 128 x 512 (two waves of
+// clusters of 8) 147 on 8 and 76 on 4.
 //
 // A stack of many matrices that need large clusters is left to the chain of
 // launches, whose time is about 20 us a step for its latencies and its padded
-// products at 0.8 PFLOP/s: 48 x 128 x 2048 takes 631 us here and 505 there,
-// 48 x 64 x 2048 221 here and 407 there.
+// products at 0.8 PFLOP/s: 48 x 128 x 2048 takes 620 us here and 429 there,
+// 48 x 64 x 2048 156 here and 342 there.
 bool resident_fits(int64_t rows, int64_t cols, int64_t count, int T, int planes, int* C_out) {
   const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
   if (n > res::MAX_N || m > res::MAX_M) return false;

@@ -596,7 +596,8 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
 def stack_params(mu: float = 0.95, lr: float = 0.02, weight_decay: float = 0.0, scale: float = 1.0, nesterov: bool = False,
                  ns: NsParams | None = None, dev_status=None) -> StackParams:
     """Parameters of a stack update; ns.compute may be F16X2 (two fp16 planes
-    per operand: about fp32 accuracy on the tensor cores)."""
+    per operand on the tensor cores: O off by about 1e-5 up to n = 256, 4e-5
+    at 1024 x 1024, 1e-4 at 4096 x 4096; F32 stays at 6e-6)."""
     p = StackParams()
     lib().muon_stack_params_default(C.byref(p))
     p.mu, p.lr, p.weight_decay, p.scale, p.nesterov = mu, lr, weight_decay, scale, int(nesterov)
