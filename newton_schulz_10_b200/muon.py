@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass, field
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -481,6 +482,24 @@ def _call_on(device: int, stream, fn, args, where: str) -> None:
         raise MuonError(code, where)
 
 
+def _on(stream, device):
+    """Context in which a call's own allocations come from the memory pool of
+    the stream that uses them: the caching allocator hands a freed block out
+    again in the order of the stream it was allocated on, so memory of another
+    stream may still be in use there, or be handed out while this one runs."""
+    if stream is None or device.type != "cuda":  # a tensor elsewhere is refused by the checks
+        return nullcontext()
+    import torch
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device))
+
+
+def _new(like, shape, stream):
+    if stream is None:
+        return like.new_empty(shape)
+    with _on(stream, like.device):
+        return like.new_empty(shape)
+
+
 def _grouped(where, x, y, w, offsets, dev_status):
     """The descriptor and device of a call: x (tokens, k), y (tokens, n), w (experts, n, k)."""
     try:
@@ -526,7 +545,7 @@ def grouped_matmul(x, w, offsets, out=None, dev_status=None, stream=None):
     (tokens, n) that belong to no expert keep their values."""
     if out is None:
         _need(x.dim() == 2 and w.dim() == 3, ERR_SHAPE, "grouped_matmul")
-        out = x.new_empty((x.shape[0], w.shape[1]))
+        out = _new(x, (x.shape[0], w.shape[1]), stream)
     if w.dtype != x.dtype:
         raise MuonError(ERR_DTYPE, "grouped_matmul")
     g, device = _grouped("grouped_matmul", x, out, w, offsets, dev_status)
@@ -539,7 +558,7 @@ def grouped_matmul_dx(dy, w, offsets, out=None, dev_status=None, stream=None):
     """dx[r] = dy[r] @ w[e]: the gradient of grouped_matmul for its rows."""
     if out is None:
         _need(dy.dim() == 2 and w.dim() == 3, ERR_SHAPE, "grouped_matmul_dx")
-        out = dy.new_empty((dy.shape[0], w.shape[2]))
+        out = _new(dy, (dy.shape[0], w.shape[2]), stream)
     if w.dtype != dy.dtype:
         raise MuonError(ERR_DTYPE, "grouped_matmul_dx")
     g, device = _grouped("grouped_matmul_dx", out, dy, w, offsets, dev_status)
@@ -553,17 +572,12 @@ def grouped_workspace_size(experts: int) -> int:
 
 
 def _workspace_on(stream, experts: int, device):
-    """A workspace of grouped_matmul_dw from the memory pool of the stream that
-    uses it (the caching allocator hands a freed block out again in the order
-    of the stream it was allocated on)."""
+    """A workspace of grouped_matmul_dw from the memory pool of its stream."""
     import torch
     with torch.cuda.device(device):
         n = grouped_workspace_size(experts)
-        if stream is None:
-            return workspace(n, device)
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device)
-        with torch.cuda.stream(s):
-            return workspace(n, device)
+    with _on(stream, device):
+        return workspace(n, device)
 
 
 def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float = 0.0, ws=None, dev_status=None, stream=None):
@@ -579,7 +593,8 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
         import torch
         _need(dy.dim() == 2 and x.dim() == 2, ERR_SHAPE, where)
         _need(beta == 0.0, ERR_INVALID_ARG, where)
-        out = torch.empty((experts, dy.shape[1], -(-x.shape[1] // 8) * 8), dtype=torch.float32, device=x.device)[:, :, :x.shape[1]]
+        with _on(stream, x.device):
+            out = torch.empty((experts, dy.shape[1], -(-x.shape[1] // 8) * 8), dtype=torch.float32, device=x.device)[:, :, :x.shape[1]]
     g, device = _grouped(where, x, dy, out, offsets, dev_status)
     if ws is None:
         ws = _workspace_on(stream, experts, x.device)
@@ -652,6 +667,10 @@ class StackStep:
         step = StackStep([Stack(W, M)], ...)  # no gradient tensor:
         step.accumulate(0, dy, x, offsets)    # M <- mu M + dy_e^T x_e
         step()                                # W from M
+
+    The workspace belongs to the stream that is current at construction: order
+    a call on another stream after it, and keep the object until that call has
+    run.
     """
     stacks: list
     params: StackParams
@@ -662,7 +681,7 @@ class StackStep:
     def __post_init__(self):
         where = "muon_stack_step"
         self._table = _stacks(self.stacks, where)
-        self._grouped_ws = [None] * len(self.stacks)
+        self._grouped_ws = [{} for _ in self.stacks]
         if self.ws is None:
             import torch
             device = self.stacks[0].W.device if self.stacks else "cuda"
@@ -685,9 +704,14 @@ class StackStep:
         the momentum step straight from an expert layer's rows."""
         k = self.stacks[i]
         _need(k.G is None, ERR_INVALID_ARG, "StackStep.accumulate")
-        if self._grouped_ws[i] is None:
-            self._grouped_ws[i] = _workspace_on(stream, k.M.shape[0], k.M.device)
-        grouped_matmul_dw(dy, x, offsets, out=k.M, beta=self.params.mu, ws=self._grouped_ws[i], stream=stream)
+        if stream is None:
+            raw = (_T or _torch())[4](k.M.get_device())
+        else:
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        kept = self._grouped_ws[i]  # one per stream, all kept: a captured graph may hold any of them
+        if raw not in kept:
+            kept[raw] = _workspace_on(stream, k.M.shape[0], k.M.device)
+        grouped_matmul_dw(dy, x, offsets, out=k.M, beta=self.params.mu, ws=kept[raw], stream=stream)
 
     def device_status(self) -> int:
         """Deferred device status of the last step (synchronises)."""
@@ -700,6 +724,12 @@ class StackStep:
 def stack_step(stacks, p: StackParams | None = None, ws=None, stream=None) -> StackStep:
     """One update of stacks = [Stack(W, M, G[, copy]), ...]. Returns the
     StackStep (reusable)."""
-    s = StackStep(list(stacks), p or stack_params(), ws)
+    stacks = list(stacks)
+    p = p or stack_params()
+    if stream is not None and ws is None and stacks:
+        with _on(stream, stacks[0].W.device):
+            s = StackStep(stacks, p)
+    else:
+        s = StackStep(stacks, p, ws)
     s(stream)
     return s

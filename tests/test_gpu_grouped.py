@@ -396,3 +396,24 @@ def test_two_calls_at_once(cuda):
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("which", ["y", "dx", "dw"])
+def test_results_on_another_stream_are_its_own(cuda, which):
+    """A result that a call makes for itself does not take memory that this stream still reads."""
+    d = torch.bfloat16
+    x, w, off = draw((512, 256), 1.0, d, 1), draw((2, 256, 256), 0.1, d, 2), offsets_of([300, 212])
+    call = {"y": lambda **k: mu.grouped_matmul(x, w, off, **k), "dx": lambda **k: mu.grouped_matmul_dx(x, w, off, **k),
+            "dw": lambda **k: mu.grouped_matmul_dw(x, x, off, **k)}[which]
+    want = call()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        old = torch.ones_like(want)
+        s.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(20_000_000)  # this stream is some milliseconds behind
+        read = old.clone()
+        del old
+        got = call(stream=stream)
+        torch.cuda.synchronize()
+        assert bool((read == 1).all()) and torch.equal(got, want)

@@ -373,3 +373,51 @@ def test_accumulate_needs_no_gradient_and_nesterov_needs_one(cuda):
     with pytest.raises(mu.MuonError) as err:
         mu.StackStep([mu.Stack(W, M)], mu.stack_params(nesterov=True))()
     assert err.value.code == mu.ERR_INVALID_ARG
+
+
+def test_workspace_of_a_step_on_another_stream(cuda):
+    """stack_step makes its workspace for the stream it runs on: the result may be dropped at once, and memory freed on
+    this stream is not written while this stream still reads it."""
+    p = mu.stack_params(nesterov=True, ns=mu.ns_params(compute=mu.BF16))
+    shape = (3, 200, 300)
+    M, G, W = gauss(shape, 95), gauss(shape, 96), gauss(shape, 97, 0.02)
+    want, m = W.clone(), M.clone()
+    size = mu.stack_step([mu.Stack(want, m, G)], p).ws.numel()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        w, m = W.clone(), M.clone()
+        old = torch.ones(size, dtype=torch.uint8, device="cuda")
+        s.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(20_000_000)  # this stream is some milliseconds behind
+        read = old.clone()
+        del old
+        mu.stack_step([mu.Stack(w, m, G)], p, stream=stream)
+        torch.cuda.synchronize()
+        assert bool((read == 1).all()) and torch.equal(w, want)
+        w, m = W.clone(), M.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        mu.stack_step([mu.Stack(w, m, G)], p, stream=stream)
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")  # would land in a workspace freed on this stream
+        torch.cuda.synchronize()
+        assert torch.equal(w, want)
+
+
+def test_accumulate_on_two_streams(cuda):
+    """Each stream has its own workspace, kept while the step lives."""
+    x, dy = gauss((4000, 128), 1, dtype=torch.bfloat16), gauss((4000, 128), 2, dtype=torch.bfloat16)
+    off = torch.tensor([0, 3000, 4000], dtype=torch.int32, device="cuda")
+    M = torch.zeros((2, 128, 128), device="cuda")
+    step = mu.StackStep([mu.Stack(torch.zeros_like(M), M)], mu.stack_params())
+    want = torch.zeros_like(M)
+    s = torch.cuda.Stream()
+    for stream in (None, s, None, s.cuda_stream):
+        mu.grouped_matmul_dw(dy, x, off, out=want, beta=step.params.mu)
+        s.wait_stream(torch.cuda.current_stream())
+        step.accumulate(0, dy, x, off, stream=stream)
+        torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    assert torch.equal(M, want)
+    assert len(step._grouped_ws[0]) == 2
