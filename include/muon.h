@@ -365,9 +365,9 @@ muon_status muon_step_events(const muon_matrix* mats, int32_t count, const muon_
  *              expert may be empty; rows before offsets[0] and from
  *              offsets[experts] on belong to no expert: they are not read,
  *              and the rows of y or dx at these places keep their values. An
- *              entry out of range or smaller than the one before is clamped
- *              and reported as MUON_ERR_INVALID_ARG to dev_status (the
- *              results are then unspecified, but no access leaves its matrix)
+ *              entry out of range or smaller than the one before is reported
+ *              as MUON_ERR_INVALID_ARG to dev_status: y and dx then keep their
+ *              values, dW is unspecified, and no access leaves its matrix
  *   dev_status optional device int32 for deferred errors, not cleared by the
  *              library (as in muon_params)
  * Outputs may not alias inputs. A row's result depends on its own row and its
@@ -421,7 +421,8 @@ muon_status grouped_matmul_dw(const muon_grouped* g, const void* dy, const void*
  * every array, a multiple of 4 columns, run faster). The matrices of W, M and
  * copy may not overlap: they follow one another (stride >= (rows-1) ld + cols)
  * or lie side by side in wider rows (ld >= (count-1) stride + cols);
- * MUON_ERR_SHAPE otherwise. G may repeat (strides of 0). w_ld and the others
+ * MUON_ERR_SHAPE otherwise. The four arrays are distinct (not checked). G may
+ * repeat (strides of 0). w_ld and the others
  * are not read for a single row, strides not for a single matrix. At most
  * 65535 matrices a stack. */
 typedef struct {

@@ -405,7 +405,9 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       if (lane >= o) incl += y;
     }
     if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
+    // Offsets that decrease could own more rows than there are, and the sum of
+    // their tiles leave 32 bits: nothing is computed for a table that is wrong.
+    const bool wrong = __syncthreads_or(bad);
     int base = incl - sum, all = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
       if (w < warp) base += wsum[w];
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
       base += c[i];
     }
     __syncthreads();
-    total = all * mt;
+    total = wrong ? 0 : all * mt;
   } else {
     total = p.experts * mt * ntl * p.splits;
   }

@@ -417,3 +417,14 @@ def test_results_on_another_stream_are_its_own(cuda, which):
         got = call(stream=stream)
         torch.cuda.synchronize()
         assert bool((read == 1).all()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("bad", [[0, 40, 0, 40], [0, 30, 20, 40], [-1, 10, 20, 30], [0, 10, 20, 41]])
+def test_bad_offsets_leave_the_rows_alone(cuda, bad):
+    d = torch.float16
+    x, w = draw((40, 64), 1.0, d, 1), draw((3, 64, 64), 0.1, d, 2)
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    for call in (mu.grouped_matmul, mu.grouped_matmul_dx):
+        y, status = torch.full_like(x, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(x, w, off, out=y, dev_status=status)
+        assert int(status.item()) == mu.ERR_INVALID_ARG and bool((y == 7.0).all())
