@@ -559,6 +559,10 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
     uint32_t acc_phase = 0;
     uint32_t old_phase = 0;  // DW: bit b is the parity of this warp's buffer b
     uint32_t in_flight = 0;  // DW, lane 0: buffers whose block was asked for and not waited for
+    // DW: the buffer that the last bulk store did not leave from. A block that
+    // is not added to takes it, from tile to tile: one store may still read
+    // its source then, and that is the other buffer.
+    uint32_t next_buf = 0;
     bool go = true;
     for (int tile = unit; tile < total && go; tile += units) {
       const Tile t = decode<MODE, NT>(p, table, tile, mt, ntl);
@@ -640,7 +644,9 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
         } else {
           // block: lanes = rows of dW_e (or of a part's 256 x 256), columns = its columns
           for (int n = 0; n < blocks; ++n) {
-            uint8_t* const buf = sd + (n & 1) * Cf::EPI_BLOCK;
+            const uint32_t b = adds ? (uint32_t)(n & 1) : next_buf;  // blocks to add to arrive in turn from buffer 0
+            uint8_t* const buf = sd + b * Cf::EPI_BLOCK;
+            next_buf = b ^ 1u;
             uint32_t raw[32];
             if (t.nkb > 0) {
               tmem_ld_32x32(trow + half * 32 + 64 * n, raw);
@@ -654,7 +660,6 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
             for (int x = 0; x < 32; ++x) v[x] = p.alpha * __uint_as_float(raw[x]);
             constexpr int V = 16 / sizeof(O);
             if (adds) {
-              const uint32_t b = (uint32_t)(n & 1);
               const bool here = mbar_wait_bounded(&olds[2 * e + b], (old_phase >> b) & 1, abort_flag, budget, p.status);
               go = __all_sync(0xffffffffu, here);
               if (!go) {

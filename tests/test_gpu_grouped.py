@@ -428,3 +428,30 @@ def test_bad_offsets_leave_the_rows_alone(cuda, bad):
         y, status = torch.full_like(x, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
         call(x, w, off, out=y, dev_status=status)
         assert int(status.item()) == mu.ERR_INVALID_ARG and bool((y == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f16", "f32"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("k", [40, 64, 91, 200, 1032])
+def test_many_tiles_with_an_odd_number_of_blocks(cuda, k, dtype, out):
+    """Several tiles a CTA pair, whose last one leaves each storing warp an odd number of 32-column blocks (1 or 3; none
+    for one half of the warps at k = 1032), with empty, short and long experts in turn: the blocks of a tile may not
+    overwrite those of the tile before while they are being stored. Repeated, since that would depend on timing."""
+    d = DT[dtype]
+    o = torch.float32 if out == "f32" else d
+    n, c = 1024, [0, 1, 0, 0, 70, 1600, 33, 0] * 8
+    off = offsets_of(c)
+    total = sum(c)
+    x, dy = draw((total, k), 1.0, d, 1), draw((total, n), 1.0, d, 2)
+    first = mu.grouped_matmul_dw(dy, x, off, out=draw((len(c), n, k), 1.0, o, 3))
+    at = off.tolist()
+    for e in range(len(c)):
+        r = slice(at[e], at[e + 1])
+        want, mag = dy[r].double().T @ x[r].double(), dy[r].double().abs().T @ x[r].double().abs()
+        tol = (half_step(o) + 2.0 ** -22) * want.abs() + 1.01 * (c[e] / 16 + 8) * 2.0 ** -23 * mag
+        tol += 2.0 ** -25 if o == torch.float16 else 0.0
+        assert bool(((first[e].double() - want).abs() <= tol).all()), e
+    ws, again = mu.workspace(mu.grouped_workspace_size(len(c))), draw((len(c), n, k), 1.0, o, 4)
+    for _ in range(20):
+        again.fill_(float("nan"))
+        mu.grouped_matmul_dw(dy, x, off, out=again, ws=ws)
+        assert torch.equal(again, first)
