@@ -15,7 +15,8 @@
 // receives its np / C rows of every partial result, adds them in rank order
 // and copies its rows of the operand to every CTA. Both arrive on mbarriers,
 // so the loop has no cluster barrier; that copies may land is implied by what
-// has arrived (below). Element-wise remote stores took 1500 to 5900 cycles a
+// has arrived (below), and a sender waits until its copies have read their
+// source before it writes there. Element-wise remote stores took 1500 to 5900 cycles a
 // step where these take a few hundred. Folding a X into B' saves reading X back
 // in the epilogue.
 //
@@ -509,8 +510,13 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
         const uint32_t o = a_a + (i - to * pieces) * group + rank * rows_per * 128;
         copy_cluster(mapa_shared(o, (uint32_t)to), o, (uint32_t)(rows_per * 128), mapa_shared(smem_u32(rows), (uint32_t)to));
       }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       if (tid == 0) mbar_complete_tx(rows, (uint32_t)(pieces * rows_per * 128));  // its own are there
       wait_for(rows, odd);
+      // What has arrived says nothing of what this thread has sent: B' takes the
+      // place of these rows once every copy has read them (the barrier ahead of
+      // the next product makes that every thread's).
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     // B' = a I + b A + c A A, in A's place (every thread rewrites what it read)
     products([&](uint32_t on) {

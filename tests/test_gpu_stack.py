@@ -422,3 +422,29 @@ def test_accumulate_on_two_streams(cuda):
     torch.cuda.synchronize()
     assert torch.equal(M, want)
     assert len(step._grouped_ws[0]) == 2
+
+
+@pytest.mark.parametrize("compute", [mu.F16X2, mu.BF16, mu.F16])
+@pytest.mark.parametrize("shape", [(1, 16, 2048), (9, 16, 1030), (40, 2048, 16), (12, 64, 768), (3, 100, 1000), (1, 128, 2048)], ids=str)
+def test_clusters_repeat_their_results(cuda, shape, compute):
+    """The CTAs of a cluster pass rows of A to one another and then write B' in their place: no peer may receive B' for A.
+    Repeated beside another stream's traffic, since that would depend on timing: the same bits every time, and right."""
+    M = spectrum(shape, 111, 1e-3) if compute == mu.F16X2 else gauss(shape, 111, 1e-3)
+    W = torch.zeros(shape, device="cuda")
+    step = mu.StackStep([mu.Stack(W, M)], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(compute=compute)))
+    before = mu.kernel_launch_count()
+    step()
+    assert mu.kernel_launch_count() - before == 1 and step.device_status() == mu.OK
+    want = polar(M)
+    for i in range(shape[0]):
+        assert rel(W[i], want[i]) <= TOL[compute], i
+    first, other = W.clone(), torch.cuda.Stream()
+    a, b = torch.zeros(1 << 24, device="cuda"), torch.zeros(1 << 24, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(60):
+        if i % 4 == 0:
+            with torch.cuda.stream(other):
+                b.copy_(a)
+        W.zero_()
+        step()
+        assert torch.equal(W, first), i
