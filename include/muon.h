@@ -355,7 +355,7 @@ muon_status muon_step_events(const muon_matrix* mats, int32_t count, const muon_
  *   dtype      BF16 or F16: type of x, W, y, dy and dx; sums are fp32 and each
  *              result is rounded once
  *   experts    0..1024
- *   tokens     rows of x and y (0..2^31 - 1); n, k >= 1
+ *   tokens     rows of x and y, at most 2^31 - 513; n, k from 1, at most the same
  *   ldx        row stride of x and dx (>= k), ldy of y and dy (>= n), ldw of
  *              W_e (>= k), w_stride from expert to expert (>= (n-1) ldw + k;
  *              not read when there is one), all in elements. Data pointers

@@ -930,7 +930,8 @@ muon_status check_grouped(const muon_grouped* g, int w_bytes, Op* t) {
   if (!g) return MUON_ERR_INVALID_ARG;
   if (g->dtype != MUON_BF16 && g->dtype != MUON_F16) return MUON_ERR_DTYPE;
   op_of(g->dtype, t);
-  if (g->experts < 0 || g->experts > grouped_max_experts() || g->tokens < 0 || g->tokens > INT32_MAX || g->n < 1 ||
+  // row and column numbers are 32 bits in the kernels and are rounded up to tiles of at most 256
+  if (g->experts < 0 || g->experts > grouped_max_experts() || g->tokens < 0 || g->tokens > INT32_MAX - 512 || g->n < 1 ||
       g->k < 1 || g->n > INT32_MAX - 512 || g->k > INT32_MAX - 512)
     return MUON_ERR_SHAPE;
   if (g->ldx < g->k || g->ldy < g->n || g->ldw < g->k) return MUON_ERR_SHAPE;

@@ -455,3 +455,47 @@ def test_many_tiles_with_an_odd_number_of_blocks(cuda, k, dtype, out):
         again.fill_(float("nan"))
         mu.grouped_matmul_dw(dy, x, off, out=again, ws=ws)
         assert torch.equal(again, first)
+
+
+def test_as_many_rows_as_fit_32_bits(cuda):
+    """2^31 - 513 rows, nearly all of them one expert's: the same 2^20 rows of x and dy over and over."""
+    d = torch.bfloat16
+    total, block, width = 2 ** 31 - 513, 1 << 20, 8
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 4 * 2 * width * total:
+        pytest.skip("needs 140 GB")
+    base_x, base_dy, w = draw((block, width), 1.0, d, 1), draw((block, width), 1.0, d, 2), draw((3, width, width), 0.5, d, 3)
+    cut = [0, 5, total - 70, total - 7]
+    off = torch.tensor(cut, dtype=torch.int32, device="cuda")
+    x, dy, out = (torch.empty((total, width), dtype=d, device="cuda") for _ in range(3))
+    for t, base in ((x, base_x), (dy, base_dy)):
+        for r in range(0, total, block):
+            t[r:r + block] = base[:total - r]
+    for call, src, transpose in ((mu.grouped_matmul, x, True), (mu.grouped_matmul_dx, dy, False)):
+        out[total - 7:] = 3.0
+        call(src, w, off, out=out)
+        assert bool((out[total - 7:] == 3.0).all())
+        for e in range(3):
+            W = w[e].double().T if transpose else w[e].double()
+            for r in range(cut[e], cut[e + 1], block * 300 + 12345):  # here and there, and the end
+                for a in (r, max(cut[e], cut[e + 1] - 4096)):
+                    rows = slice(a, min(a + 4096, cut[e + 1]))
+                    close(out[rows], src[rows].double() @ W, src[rows].double().abs() @ W.abs(), width, d)
+    del out
+    dw = mu.grouped_matmul_dw(dy, x, off)
+    whole = base_dy.double().T @ base_x.double()
+    left = total % block
+    want = (total // block) * whole + base_dy[:left].double().T @ base_x[:left].double()
+    ends = [dy[a:b].double().T @ x[a:b].double() for a, b in ((0, 5), (total - 70, total - 7))]
+    tail = dy[total - 7:].double().T @ x[total - 7:].double()
+    want = torch.stack([ends[0], want - ends[0] - ends[1] - tail, ends[1]])
+    # sums of at most 768 rows as elsewhere; then at most 2^28 / 768 additions of them, rounded to nearest (half a step of a
+    # sum that is largest at the end), and one for each of at most 16 parts
+    adds = (total / 16 + 64) / 768 + 16
+    mag = torch.stack([ends[0].abs(), (total // block + 1) * (base_dy.double().abs().T @ base_x.double().abs()), ends[1].abs()])
+    mag[0], mag[2] = dy[:5].double().abs().T @ x[:5].double().abs(), dy[total - 70:total - 7].double().abs().T @ x[total - 70:total - 7].double().abs()
+    tol = (768 / 16 + 8) * 2.0 ** -23 * mag + adds * 2.0 ** -24 * want.abs().max()
+    assert bool(((dw.double() - want).abs() <= tol).all())
+    assert ((dw[1].double() - want[1]).norm() <= 0.05 * want[1].norm())
+    del x, dy
+    torch.cuda.empty_cache()

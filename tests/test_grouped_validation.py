@@ -117,3 +117,12 @@ def test_binding_refuses_wrong_tensors(L):
         with pytest.raises(mu.MuonError) as err:
             call()
         assert err.value.code == code, i
+
+
+@pytest.mark.parametrize("tokens", [2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 255, 2 ** 31 - 512])
+def test_rows_whose_tiles_leave_32_bits_are_refused(L, tokens):
+    """Row numbers rounded up to a tile, or to a block of 64, have to stay within 32 bits."""
+    g = desc(tokens=tokens, n=8, k=8, ldx=8, ldy=8, ldw=8, w_stride=64)
+    for call in (L.grouped_matmul, L.grouped_matmul_dx):
+        assert call(C.byref(g), FAKE, FAKE, FAKE, None) == mu.ERR_SHAPE
+    assert L.grouped_matmul_dw(C.byref(g), FAKE, FAKE, FAKE, mu.F32, 1.0, 0.0, FAKE, 1 << 30, None) == mu.ERR_SHAPE
