@@ -598,9 +598,13 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
     g, device = _grouped(where, x, dy, out, offsets, dev_status)
     if ws is None:
         ws = _workspace_on(stream, experts, x.device)
+    _call_dw(where, g, device, dy, x, out, alpha, beta, ws, stream)
+    return out
+
+
+def _call_dw(where, g, device, dy, x, out, alpha, beta, ws, stream):
     _call_on(device, stream, (_lib or lib()).grouped_matmul_dw, (C.byref(g), dy.data_ptr(), x.data_ptr(), out.data_ptr(),
                                                        _code_of(out, where), alpha, beta, ws.data_ptr(), ws.numel()), where)
-    return out
 
 
 # ---------------------------------------------------------------------------
@@ -677,11 +681,15 @@ class StackStep:
     ws: object = None
     _table: object = field(default=None, repr=False)
     _grouped_ws: list = field(default=None, repr=False)
+    _deferred: object = field(default=None, repr=False)  # status word of the accumulate calls
 
     def __post_init__(self):
         where = "muon_stack_step"
         self._table = _stacks(self.stacks, where)
         self._grouped_ws = [{} for _ in self.stacks]
+        if any(k.G is None for k in self.stacks):
+            import torch
+            self._deferred = torch.zeros(1, dtype=torch.int32, device=self.stacks[0].W.device)
         if self.ws is None:
             import torch
             device = self.stacks[0].W.device if self.stacks else "cuda"
@@ -701,23 +709,36 @@ class StackStep:
 
     def accumulate(self, i: int, dy, x, offsets, stream=None) -> None:
         """M <- mu M + dy_e^T x_e for the experts of stack i, whose G is None:
-        the momentum step straight from an expert layer's rows."""
+        the momentum step straight from an expert layer's rows. Deferred
+        errors (offsets out of order, a wait that ran out) go to the
+        parameters' dev_status, else to device_status()."""
+        where = "StackStep.accumulate"
         k = self.stacks[i]
-        _need(k.G is None, ERR_INVALID_ARG, "StackStep.accumulate")
+        _need(k.G is None, ERR_INVALID_ARG, where)
         if stream is None:
             raw = (_T or _torch())[4](k.M.get_device())
         else:
             raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        g, device = _grouped(where, x, dy, k.M, offsets, None)
+        g.dev_status = self.params.dev_status or self._deferred.data_ptr()
         kept = self._grouped_ws[i]  # one per stream, all kept: a captured graph may hold any of them
         if raw not in kept:
             kept[raw] = _workspace_on(stream, k.M.shape[0], k.M.device)
-        grouped_matmul_dw(dy, x, offsets, out=k.M, beta=self.params.mu, ws=kept[raw], stream=stream)
+        _call_dw(where, g, device, dy, x, k.M, 1.0, self.params.mu, kept[raw], stream)
 
     def device_status(self) -> int:
-        """Deferred device status of the last step (synchronises)."""
+        """Deferred device status of the last step (synchronises). An error of
+        accumulate comes first and is kept until it has been returned here:
+        the momentum that it left unspecified outlives the step."""
         import torch
         if self.params.dev_status:
             raise RuntimeError("status goes to the caller's dev_status")
+        if self._deferred is not None:
+            torch.cuda.synchronize(self._deferred.device)  # accumulate may have run on any stream
+            code = int(self._deferred.item())
+            if code != OK:
+                self._deferred.zero_()
+                return code
         return int(self.ws[:4].view(torch.int32).item())
 
 

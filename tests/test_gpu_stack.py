@@ -448,3 +448,36 @@ def test_clusters_repeat_their_results(cuda, shape, compute):
         W.zero_()
         step()
         assert torch.equal(W, first), i
+
+
+@pytest.mark.parametrize("own_word", [False, True])
+@pytest.mark.parametrize("bad", [[0, 40, 20, 60], [0, 20, 40, 61], [-1, 20, 40, 60]])
+def test_deferred_errors_of_accumulate(cuda, bad, own_word):
+    """Offsets out of order leave the momentum unspecified: reported where the step's errors are, and not forgotten by
+    the step that follows."""
+    dy, x = gauss((60, 24), 1, dtype=torch.bfloat16), gauss((60, 40), 2, dtype=torch.bfloat16)
+    good = torch.tensor([0, 20, 40, 60], dtype=torch.int32, device="cuda")
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    M = torch.zeros((3, 24, 40), device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda") if own_word else None
+    step = mu.StackStep([mu.Stack(torch.zeros_like(M), M)], mu.stack_params(dev_status=word))
+
+    def status():
+        if not own_word:
+            return step.device_status()
+        code = int(word.item())
+        word.zero_()
+        return code
+
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        for table, code in ((good, mu.OK), (off, mu.ERR_INVALID_ARG), (good, mu.OK)):
+            M.zero_()
+            side.wait_stream(torch.cuda.current_stream())
+            step.accumulate(0, dy, x, table, stream=stream)
+            torch.cuda.current_stream().wait_stream(side)
+            if code != mu.OK:
+                M.zero_()  # unspecified, NaN perhaps; the step has errors of its own to tell
+            step()
+            assert status() == code
+            assert status() == mu.OK
