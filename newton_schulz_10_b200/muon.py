@@ -571,6 +571,13 @@ def grouped_workspace_size(experts: int) -> int:
     return lib().grouped_workspace_size(experts)
 
 
+def _ws_bytes(ws, device: int, where: str) -> int:
+    """Bytes of a workspace, which has to be one piece of the device's memory."""
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise MuonError(ERR_INVALID_ARG, where)
+    return ws.numel() * ws.element_size()
+
+
 def _workspace_on(stream, experts: int, device):
     """A workspace of grouped_matmul_dw from the memory pool of its stream."""
     import torch
@@ -603,8 +610,9 @@ def grouped_matmul_dw(dy, x, offsets, out=None, alpha: float = 1.0, beta: float 
 
 
 def _call_dw(where, g, device, dy, x, out, alpha, beta, ws, stream):
+    size = _ws_bytes(ws, device, where)
     _call_on(device, stream, (_lib or lib()).grouped_matmul_dw, (C.byref(g), dy.data_ptr(), x.data_ptr(), out.data_ptr(),
-                                                       _code_of(out, where), alpha, beta, ws.data_ptr(), ws.numel()), where)
+                                                       _code_of(out, where), alpha, beta, ws.data_ptr(), size), where)
 
 
 # ---------------------------------------------------------------------------
@@ -622,7 +630,11 @@ def stack_params(mu: float = 0.95, lr: float = 0.02, weight_decay: float = 0.0, 
     p.mu, p.lr, p.weight_decay, p.scale, p.nesterov = mu, lr, weight_decay, scale, int(nesterov)
     if ns is not None:
         p.ns = ns
-    p.dev_status = None if dev_status is None else _ptr(dev_status)
+    if dev_status is not None:
+        import torch
+        _need(dev_status.is_cuda and dev_status.dtype == torch.int32 and dev_status.numel() >= 1, ERR_INVALID_ARG, "stack_params")
+        p.dev_status = _ptr(dev_status)
+        p.status_tensor = dev_status  # lives as long as the parameters that hold its address
     return p
 
 
@@ -700,12 +712,17 @@ class StackStep:
             else:
                 n = 0
             self.ws = workspace(n, device)
+        if self.stacks:
+            device = self.stacks[0].W.get_device()
+            status = getattr(self.params, "status_tensor", None)
+            _need(status is None or status.get_device() == device, ERR_INVALID_ARG, where)
+            self._ws_bytes = _ws_bytes(self.ws, device, where)
 
     def __call__(self, stream=None) -> None:
         if not self.stacks:
             return
         _call_on(self.stacks[0].W.get_device(), stream, lib().muon_stack_step,
-                 (self._table, len(self.stacks), C.byref(self.params), _ptr(self.ws), self.ws.numel()), "muon_stack_step")
+                 (self._table, len(self.stacks), C.byref(self.params), _ptr(self.ws), self._ws_bytes), "muon_stack_step")
 
     def accumulate(self, i: int, dy, x, offsets, stream=None) -> None:
         """M <- mu M + dy_e^T x_e for the experts of stack i, whose G is None:
@@ -739,7 +756,7 @@ class StackStep:
             if code != OK:
                 self._deferred.zero_()
                 return code
-        return int(self.ws[:4].view(torch.int32).item())
+        return int(self.ws.view(-1).view(torch.uint8)[:4].view(torch.int32).item())
 
 
 def stack_step(stacks, p: StackParams | None = None, ws=None, stream=None) -> StackStep:

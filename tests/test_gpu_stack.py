@@ -481,3 +481,33 @@ def test_deferred_errors_of_accumulate(cuda, bad, own_word):
             step()
             assert status() == code
             assert status() == mu.OK
+
+
+def test_workspaces_and_status_words_of_calls(cuda):
+    """A workspace on the host or in pieces is refused; one of another element type counts its bytes; a status word
+    lives as long as the parameters that hold its address."""
+    import gc
+    import weakref
+    M, x, off = gauss((2, 16, 24), 1), gauss((5, 24), 2, dtype=torch.bfloat16), torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    need = mu.grouped_workspace_size(2)
+    pieces = torch.empty((need // 4 + 1, 8), dtype=torch.uint8, device="cuda")[:, :4]
+    for ws in (torch.empty(need, dtype=torch.uint8), pieces):
+        for call in (lambda: mu.grouped_matmul_dw(x, x, off, ws=ws), lambda: mu.StackStep([mu.Stack(M.clone(), M.clone())], mu.stack_params(), ws=ws)):
+            with pytest.raises(mu.MuonError) as err:
+                call()
+            assert err.value.code == mu.ERR_INVALID_ARG
+    want = mu.grouped_matmul_dw(x, x, off)
+    assert torch.equal(mu.grouped_matmul_dw(x, x, off, ws=torch.empty(need // 4 + 1, dtype=torch.float32, device="cuda")), want)
+    a, b = M.clone(), M.clone()
+    size = mu.stack_step([mu.Stack(a, M.clone())]).ws.numel()
+    step = mu.StackStep([mu.Stack(b, M.clone())], mu.stack_params(), ws=torch.empty(size // 2 + 1, dtype=torch.float16, device="cuda"))
+    step()
+    assert step.device_status() == mu.OK and torch.equal(a, b)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    alive, p = weakref.ref(word), mu.stack_params(dev_status=word)
+    step = mu.StackStep([mu.Stack(b, M.clone())], p)
+    del word, p
+    gc.collect()
+    assert alive() is not None
+    step()
+    assert int(alive().item()) == mu.OK

@@ -145,3 +145,16 @@ def test_binding_refuses_wrong_tensors(L):
         with pytest.raises(mu.MuonError) as err:
             f()
         assert err.value.code == code, i
+
+
+def test_status_words_and_workspaces_elsewhere_are_refused(L):
+    """The kernels write to both: memory of the host, of another type or in pieces is refused before any launch."""
+    for word in (torch.zeros(1, dtype=torch.int32), torch.zeros(1)):
+        with pytest.raises(mu.MuonError) as err:
+            mu.stack_params(dev_status=word)
+        assert err.value.code == mu.ERR_INVALID_ARG
+    for device, ws in ((0, torch.zeros(64, dtype=torch.uint8)), (-1, torch.zeros(8, 8, dtype=torch.uint8)[:, :4])):
+        with pytest.raises(mu.MuonError) as err:
+            mu._ws_bytes(ws, device, "here")
+        assert err.value.code == mu.ERR_INVALID_ARG
+    assert mu._ws_bytes(torch.zeros(8, 8), -1, "here") == 256
