@@ -451,7 +451,9 @@ typedef struct {
  *   ns            compute may be MUON_F16X2 (gram = 0 only, else
  *                 MUON_ERR_UNSUPPORTED). Its operands, and fp16's, are scaled
  *                 for coefficients up to 15 in magnitude; a polynomial that
- *                 leaves fp16's range is reported as MUON_ERR_NONFINITE
+ *                 leaves fp16's range is reported as MUON_ERR_NONFINITE, and
+ *                 so is a bf16 matrix whose norm's square leaves fp32's (norms
+ *                 up to 1e18 are safe)
  *   dev_status    as in muon_params */
 typedef struct {
   float mu;

@@ -1145,8 +1145,10 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
 
   // bf16 operands are stored unscaled, in the momentum pass itself, and the
   // Frobenius scale enters the first products; the others are scaled once
-  // the norm is known.
-  const bool folded = planes == 1 && t == Op::BF16;
+  // the norm is known. So are bf16's with an eps next to 0, which leaves the
+  // scale of a tiny matrix unbounded: its square, which scales the first
+  // product, would leave fp32's range (and the product itself would be 0).
+  const bool folded = planes == 1 && t == Op::BF16 && ns.norm_eps >= 1e-12f;
   StackLaunch proto;
   memset(&proto, 0, sizeof(proto));
   proto.mu = p->mu;

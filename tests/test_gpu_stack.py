@@ -511,3 +511,37 @@ def test_workspaces_and_status_words_of_calls(cuda):
     assert alive() is not None
     step()
     assert int(alive().item()) == mu.OK
+
+
+@pytest.mark.parametrize("compute", [mu.F16X2, mu.BF16, mu.F16, mu.F32])
+@pytest.mark.parametrize("shape", [(6, 136, 300), (6, 300, 136)], ids=str)
+def test_range_of_the_chain(cuda, shape, compute):
+    """Matrices too large for the chip: zeros are left alone (with eps 0 too), a tiny or huge matrix is orthogonalised like
+    any other, down to entries whose squares leave fp32's range. bf16's range ends at a norm of 1e18."""
+    M = gauss(shape, 121)
+    M[1] = 0
+    M[2] *= 1e-6
+    M[3] *= 1e15 if compute == mu.BF16 else 1e30
+    M[4] = 0
+    M[4, 3, 5] = 2.0
+    for eps, tiny in ((1e-7, 1e-21), (0.0, 1e-16), (0.0, 1e-21), (0.0, 1e-25), (0.0, 1e-33)):
+        M[5] = gauss(shape[1:], 122) * tiny
+        W = torch.ones_like(M)
+        step = mu.stack_step([mu.Stack(W, M.clone())], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(compute=compute, norm_eps=eps)))
+        assert step.device_status() == mu.OK, (eps, tiny)
+        assert bool((W[1] == 1).all())
+        want = polar(M, eps)
+        for i in (0, 2, 3, 4, 5):
+            # 1 + O in fp32: half a step of 1 an element beside O's own error
+            off = (W[i].double() - 1 - want[i]).norm()
+            assert off <= TOL[compute] * want[i].norm() + 2.0 ** -23 * math.sqrt(shape[1] * shape[2]), (eps, tiny, i)
+
+
+def test_large_bf16_matrix_is_reported(cuda):
+    """The chain's bf16 operands are stored unscaled: norms from 1e18 on may be reported (from 1e20 on they are)."""
+    M = gauss((2, 200, 300), 123)
+    M[1] *= 1e20
+    W = torch.zeros_like(M)
+    step = mu.stack_step([mu.Stack(W, M.clone())], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(compute=mu.BF16)))
+    assert step.device_status() == mu.ERR_NONFINITE
+    assert rel(W[0], polar(M[0])) <= TOL[mu.BF16]
