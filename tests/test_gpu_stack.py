@@ -545,3 +545,61 @@ def test_large_bf16_matrix_is_reported(cuda):
     step = mu.stack_step([mu.Stack(W, M.clone())], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(compute=mu.BF16)))
     assert step.device_status() == mu.ERR_NONFINITE
     assert rel(W[0], polar(M[0])) <= TOL[mu.BF16]
+
+
+@pytest.mark.parametrize("compute", [mu.F16X2, mu.BF16, mu.F16, mu.F32])
+def test_nonfinite_matrix_stays_alone_in_the_chain(cuda, compute):
+    M = gauss((3, 200, 300), 124)
+    W = gauss(M.shape, 125)
+    p = mu.stack_params(ns=mu.ns_params(compute=compute))
+    good = W.clone()
+    assert mu.stack_step([mu.Stack(good, M.clone())], p).device_status() == mu.OK
+    for bad in (float("nan"), float("inf")):
+        M2, W2 = M.clone(), W.clone()
+        M2[1, 3, 7] = bad
+        assert mu.stack_step([mu.Stack(W2, M2)], p).device_status() == mu.ERR_NONFINITE
+        assert torch.equal(W2[0], good[0]) and torch.equal(W2[2], good[2])
+
+
+@pytest.mark.parametrize("compute", [mu.F16, mu.BF16, mu.F32])
+@pytest.mark.parametrize("shape", [(3, 64, 200), (2, 130, 257), (2, 257, 130), (2, 24, 1000), (2, 520, 264), (1, 1, 40)], ids=str)
+def test_gram_chain_of_other_shapes(cuda, shape, compute):
+    """By the Gram iteration, which the on-chip form does not take; the last matrix is zeros. In bf16 its own storage points
+    miss 2e-2: rounding R, Q and Z where the chain stores them, and nothing else, gives 1.5e-2 to 2.5e-2 (a single row) on
+    gaussian matrices of these shapes; twice that is allowed."""
+    M = gauss(shape, 126, 1e-3)
+    if shape[0] > 1:
+        M[-1] = 0
+    W = torch.zeros_like(M)
+    step = mu.stack_step([mu.Stack(W, M.clone())], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(gram=True, compute=compute)))
+    assert step.device_status() == mu.OK
+    tol = 5e-2 if compute == mu.BF16 else TOL[compute]
+    want = polar(M)
+    for i in range(shape[0]):
+        assert rel(W[i], want[i]) <= tol if want[i].any() else not bool(W[i].any()), i
+
+
+@pytest.mark.parametrize("shape", [(8, 520, 1030), (8, 1030, 520), (32, 264, 776), (12, 776, 264), (3, 1000, 1000), (1, 1536, 2050)], ids=str)
+def test_two_planes_of_larger_stacks(cuda, shape):
+    """More tiles than one wave of the smallest holds: CTA pairs on 256 and 128 columns, several tiles a pair, several chunks
+    a storing warp, ragged edges. Besides the tolerance for small matrices the sums' own roundings count: the accumulator
+    loses up to 2^-23 of its running sum in each instruction of 16 columns, half of that on average, and 2/3 of the final
+    sum stands in it on average, so a product over K columns is off by K / 16 * 2^-23 / 3 of itself. The first product
+    (K = the longer side) and the last (the shorter) enter O about once each step, the n x n one through B, and a step
+    passes on what it gets with a factor of at most 3.44 (its slope at 0) and about 1 near the end: five steps, allowed
+    once each with factor 2."""
+    longer, shorter = max(shape[1:]), min(shape[1:])
+    M = spectrum(shape, 131, 1e-3)
+    W0, G = gauss(shape, 132, 0.02), spectrum(shape, 133, 1e-3)
+    W, Mv = W0.clone(), M.clone()
+    C = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    p = mu.stack_params(nesterov=True, weight_decay=0.1, scale=-3.0, ns=mu.ns_params(compute=mu.F16X2))
+    step = mu.stack_step([mu.Stack(W, Mv, G, C)], p)
+    assert step.device_status() == mu.OK
+    tol = TOL[mu.F16X2] + 5 * 2 * (longer + 2 * shorter) / 16 * 2.0 ** -23 / 3
+    check_update(W0, M, G, W, Mv, C, p, tol)
+    want = polar(G.double() + p.mu * Mv.double())
+    O = (W.double() - (1 - p.lr * p.weight_decay) * W0.double()) / (3.0 * p.lr)
+    for i in range(shape[0]):
+        # W's three roundings (of values below 0.125) as in test_small_matrices
+        assert rel(O[i], want[i]) <= tol + 3 * 2.0 ** -27 / 0.06 / 0.9 * math.sqrt(longer), i
