@@ -1134,7 +1134,11 @@ muon_status stack_impl(const muon_stack* st, int32_t count, const muon_stack_par
   muon_ns_params ns = p->ns;
   if (planes == 2) ns.compute = MUON_F16;
   const StackPlan q = plan_stacks(st, count, &ns, t, planes);
-  if (q.groups.empty() && q.small.empty()) return MUON_OK;
+  if (q.groups.empty() && q.small.empty()) {
+    // nothing is launched, but the status word is read all the same
+    if (!p->dev_status && ws && ws_bytes >= sizeof(int) && cudaMemsetAsync(ws, 0, sizeof(int), s) != cudaSuccess) return MUON_ERR_CUDA;
+    return MUON_OK;
+  }
   if (!ws) return MUON_ERR_WORKSPACE;
   if (!aligned16(ws)) return MUON_ERR_ALIGN;
   if (ws_bytes < q.total) return MUON_ERR_WORKSPACE;

@@ -756,6 +756,8 @@ class StackStep:
             if code != OK:
                 self._deferred.zero_()
                 return code
+        if not self.stacks:
+            return OK  # no call writes the word
         return int(self.ws.view(-1).view(torch.uint8)[:4].view(torch.int32).item())
 
 

@@ -603,3 +603,12 @@ def test_two_planes_of_larger_stacks(cuda, shape):
     for i in range(shape[0]):
         # W's three roundings (of values below 0.125) as in test_small_matrices
         assert rel(O[i], want[i]) <= tol + 3 * 2.0 ** -27 / 0.06 / 0.9 * math.sqrt(longer), i
+
+
+def test_status_of_stacks_without_elements(cuda):
+    """Nothing is computed, and the status is not what happened to be in the workspace."""
+    dirty = torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
+    for stacks in ([], [(0, 8, 8)], [(2, 0, 8), (3, 8, 0)]):
+        step = mu.StackStep([mu.Stack(gauss(s, 1), gauss(s, 2), gauss(s, 3)) for s in stacks], mu.stack_params(), ws=dirty.clone())
+        step()
+        assert step.device_status() == mu.OK
