@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "resident_model.h"
 #include "rowio.cuh"
 #include "stack.cuh"
 
@@ -53,26 +54,8 @@ namespace res {
 
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
-constexpr int MAX_N = 128;      // rows of the wide view
-constexpr int MAX_M = 2048;     // columns of the wide view
-constexpr int MAX_G = 8;        // 64-column groups per CTA (their accumulators fill TMEM)
-constexpr int MAX_C = 16;       // CTAs per cluster (above 8 only where a smaller one cannot hold the matrix)
-constexpr int MISC = 1024;
 constexpr int TMEM_COLS = 512;
 constexpr uint64_t DRAIN_NS = 1000000000ull;
-constexpr int SMEM_MAX = 232448;  // opt-in shared memory of one sm_100 CTA
-
-// A 64-column group of a plane: np rows of 128 bytes.
-constexpr int group_bytes(int np) { return np * 128; }
-// X (g groups) and A (np rows and columns), two planes each, and with a
-// cluster the np x np fp32 sums; the M side of a product reads 128 rows from
-// a group's start, so as much must lie behind the last one. At least 120 KB,
-// so that an SM holds one CTA (two would wait for each other's TMEM columns).
-constexpr int smem_bytes(int g, int np, int C) {
-  const int b = 1024 + 2 * (g + (np + 63) / 64) * group_bytes(np) + (C > 1 ? np * np * 4 : 0) + MISC + group_bytes(128 - np);
-  return b > 120 * 1024 ? b : 120 * 1024;
-}
-static_assert(smem_bytes(4, MAX_N, 1) <= SMEM_MAX && smem_bytes(2, MAX_N, MAX_C) <= SMEM_MAX, "every shape fits");
 
 struct Params {
   StackMat m;
@@ -695,80 +678,45 @@ muon_status launch_resident(const res::Params& p, cudaStream_t s) {
 
 namespace {
 
-// Clusters of C CTAs (one per SM) that can run at once on the current device.
+// Clusters of C CTAs (one per SM) that can run at once on the current device;
+// 0 where such a cluster cannot be scheduled.
 int cluster_capacity(int C) {
   static std::mutex mu;
-  static int cap[64][5];
+  static int cap[64][5];  // 0: not asked yet, -1: none
+  if (C == 1) return num_sms();
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || set_up<__half, 2>() != MUON_OK) {
     cudaGetLastError();
-    return num_sms() / C;
+    return 0;
   }
   int k = 0;
   while ((1 << k) < C) ++k;
   std::lock_guard<std::mutex> lock(mu);
   int& n = cap[dev][k];
   if (n == 0) {
-    n = num_sms() / C;
-    if (C > 1 && set_up<__half, 2>() == MUON_OK) {
-      cudaLaunchConfig_t q = {};
-      q.gridDim = dim3((unsigned)(n * C));
-      q.blockDim = dim3(res::THREADS);
-      q.dynamicSmemBytes = res::SMEM_MAX;
-      cudaLaunchAttribute a[1];
-      a[0].id = cudaLaunchAttributeClusterDimension;
-      a[0].val.clusterDim.x = (unsigned)C;
-      a[0].val.clusterDim.y = 1;
-      a[0].val.clusterDim.z = 1;
-      q.attrs = a;
-      q.numAttrs = 1;
-      int c = 0;
-      if (cudaOccupancyMaxActiveClusters(&c, res::stack_resident<__half, 2>, &q) == cudaSuccess && c > 0 && c < n) n = c;
-      cudaGetLastError();
-    }
-    if (n < 1) n = 1;
+    cudaLaunchConfig_t q = {};
+    q.gridDim = dim3((unsigned)(num_sms() / C * C));
+    q.blockDim = dim3(res::THREADS);
+    q.dynamicSmemBytes = res::SMEM_MAX;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = (unsigned)C;
+    a[0].val.clusterDim.y = 1;
+    a[0].val.clusterDim.z = 1;
+    q.attrs = a;
+    q.numAttrs = 1;
+    int c = 0;
+    const bool ok = num_sms() >= C && cudaOccupancyMaxActiveClusters(&c, res::stack_resident<__half, 2>, &q) == cudaSuccess && c > 0;
+    cudaGetLastError();
+    n = ok ? std::min(c, num_sms() / C) : -1;
   }
-  return n;
+  return std::max(n, 0);
 }
 
 }  // namespace
 
-// The cluster size, by a model of the step in cycles (measured with the clock
-// register at np = 64 and 128, g = 1 to 4, C = 1 to 8): an instruction of the
-// products takes at least 75 cycles, an epilogue 700 a group of X and 75 per
-// four rows and columns of B', the exchange 1700 + 0.55 np^2 whatever C is,
-// loads and stores 0.4 an element. Larger clusters halve the work on X and
-// pay the exchange: 12 x 64 x 768 takes 45 us on 8 CTAs a matrix and 51 on 4,
-// 1 x 128 x 128 takes 68 on 2 and 47 on 1, 16 x 128 x 512 (two waves of
-// clusters of 8) 147 on 8 and 76 on 4.
-//
-// A stack of many matrices that need large clusters is left to the chain of
-// launches, whose time is about 20 us a step for its latencies and its padded
-// products at 0.8 PFLOP/s: 48 x 128 x 2048 takes 620 us here and 429 there,
-// 48 x 64 x 2048 156 here and 342 there.
 bool resident_fits(int64_t rows, int64_t cols, int64_t count, int T, int planes, int* C_out) {
-  const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
-  if (n > res::MAX_N || m > res::MAX_M) return false;
-  const int groups = (int)((m + 63) / 64), np = (int)((n + 15) / 16 * 16);
-  double best = 0.0;
-  int best_C = 0;
-  for (int C = 1; C <= res::MAX_C; C *= 2) {
-    const int g = (groups + C - 1) / C;
-    if (g > res::MAX_G || res::smem_bytes(g, np, C) > res::SMEM_MAX) continue;
-    if (C > 8 && best_C) break;  // only where a smaller cluster cannot hold the matrix
-    const double step = 2000.0 + 900.0 * g + 14.0 * np + std::max(14.0 * np * ((g + 3) / 4), 6.6 * np * g) + 700.0 * g + 19.0 * np +
-                        (C > 1 ? 1700.0 + 0.55 * np * np : 1000.0);
-    const double waves = (double)((count + cluster_capacity(C) - 1) / cluster_capacity(C));
-    const double t = waves * (12000.0 + 0.4 * n * 64 * g + T * step);
-    if (!best_C || t < best) {
-      best = t;
-      best_C = C;
-    }
-  }
-  const double N = 256.0, tile = (double)(m + 127) / 128 * 128;
-  const double chain = 20.0 * T + 2.0 * count * T * (N * N * tile + N * N * np + N * tile * np) * (planes == 2 ? 3.0 : 1.0) / 0.8e9;
-  if (C_out) *C_out = best_C;
-  return best_C > 0 && 1.25 * best / 1850.0 <= chain;  // the model is 10 to 20% low
+  return res::choose_cluster(rows, cols, count, T, planes, cluster_capacity, C_out);
 }
 
 muon_status launch_stack_resident(const StackLaunch& L, const muon_ns_params& ns, Op t, int planes, float kappa, float rho,

@@ -158,3 +158,21 @@ def test_status_words_and_workspaces_elsewhere_are_refused(L):
             mu._ws_bytes(ws, device, "here")
         assert err.value.code == mu.ERR_INVALID_ARG
     assert mu._ws_bytes(torch.zeros(8, 8), -1, "here") == 256
+
+
+def test_clusters_that_cannot_run_are_left_out(tmp_path):
+    """A device (or a part of one) that holds no cluster of 16, or of any size: the stack goes to a smaller cluster or to
+    the chain of launches; on a whole B200 the choice is the measured one."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(mu.__file__))), "newton_schulz_10_b200", "csrc")
+    src = tmp_path / "m.cpp"
+    src.write_text('#include <stdio.h>\n#include "resident_model.h"\n'
+                   "int main(){const int most[]={16,8,4,1};const int64_t s[][3]={{1,128,2048},{12,64,768},{1,128,128},{16,128,512}};\n"
+                   "for(auto& k:s)for(int m:most){int c=-1;const bool fits=muon::res::choose_cluster(k[1],k[2],k[0],5,2,"
+                   "[m](int C){return C<=m?148/C:0;},&c);printf(\"%d %d \",(int)fits,c);}return 0;}\n")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(src), "-o", str(tmp_path / "m")], check=True)
+    got = list(map(int, subprocess.run([str(tmp_path / "m")], capture_output=True, text=True, check=True).stdout.split()))
+    choice = list(zip(got[::2], got[1::2]))
+    assert choice[:4] == [(1, 16), (0, 0), (0, 0), (0, 0)]  # 128 x 2048 fits 16 CTAs only
+    assert choice[4] == choice[5] == (1, 8) and choice[6] == (1, 4)  # 64 x 768
+    assert choice[8:12] == [(1, 1)] * 4  # 128 x 128
+    assert choice[12][0] == choice[13][0] == choice[14][0] == 1 and all(c <= 4 for _, c in choice[14:16])
