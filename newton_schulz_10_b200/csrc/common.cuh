@@ -183,19 +183,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// CTA-pair form (tcgen05 cta_group::2): the data lands in this CTA's shared
-// memory; the completion is counted on the pair leader's barrier at the same
-// offset (bit 24 of the shared::cluster address selects the CTA of the pair).
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                                 uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(c0),
-      "r"(c1), "r"(c2)
-      : "memory");
-}
-
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -244,6 +231,7 @@ __device__ __forceinline__ uint32_t elect_one() {
   return e;
 }
 // The forms below act in the lanes where `on` is not 0.
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (bf16 or fp16 in, fp32 out).
 __device__ __forceinline__ void umma_f16_if(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
@@ -254,6 +242,8 @@ __device__ __forceinline__ void umma_f16_if(uint32_t on, uint32_t d_tmem, uint64
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
+// CTA-pair MMA: D (128 rows in each CTA's TMEM) += A (128 rows from each
+// CTA's shared memory) * B (half of N from each CTA), issued by the leader.
 __device__ __forceinline__ void umma_f16_pair_if(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                                  uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -264,6 +254,8 @@ __device__ __forceinline__ void umma_f16_pair_if(uint32_t on, uint32_t d_tmem, u
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
+// Arrive on an mbarrier once every tcgen05 operation issued so far by this
+// thread has completed.
 __device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -271,6 +263,8 @@ __device__ __forceinline__ void umma_commit_if(uint32_t on, uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(on)
       : "memory");
 }
+// Completion of the pair's MMAs arrives on the barrier at this offset in
+// every CTA named in cta_mask.
 __device__ __forceinline__ void umma_commit_pair_if(uint32_t on, uint64_t* bar, uint16_t cta_mask) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -297,6 +291,9 @@ __device__ __forceinline__ void tma_load_3d_if(uint32_t on, void* dst, const CUt
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(on)
       : "memory");
 }
+// CTA-pair form (tcgen05 cta_group::2): the data lands in this CTA's shared
+// memory; the completion is counted on the pair leader's barrier at the same
+// offset (bit 24 of the shared::cluster address selects the CTA of the pair).
 __device__ __forceinline__ void tma_load_3d_pair_if(uint32_t on, void* dst, const CUtensorMap* map, int c0, int c1, int c2,
                                                     uint64_t* bar) {
   asm volatile(
@@ -339,15 +336,10 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// 32-bit stores and loads of cluster shared memory, relaxed at cluster scope
-// (the values themselves carry the information: counters and flags).
+// 32-bit store to cluster shared memory, relaxed at cluster scope (the values
+// themselves carry the information: counters and flags).
 __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
-  uint32_t v;
-  asm volatile("ld.relaxed.cluster.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
-  return v;
 }
 // Count `bytes` of transactions on a barrier as completed without a copy
 // (used only to settle a barrier whose expected copies were never issued).
@@ -367,47 +359,6 @@ __device__ __forceinline__ void tc_fence_before() {
 }
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16 (bf16 or fp16 in, fp32 out).
-__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// CTA-pair MMA: D (128 rows in each CTA's TMEM) += A (128 rows from each
-// CTA's shared memory) * B (half of N from each CTA), issued by the leader.
-__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Completion of the pair's MMAs arrives on the barrier at this offset in
-// every CTA named in cta_mask.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t cta_mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(cta_mask)
-      : "memory");
-}
-
-// Arrive on an mbarrier once every tcgen05 operation issued so far by this
-// thread has completed.
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
 }
 
 // 32 lanes x 32 consecutive fp32 columns: thread i of the warp receives lane
@@ -481,6 +432,82 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
 __host__ __device__ constexpr uint32_t idesc_f16(int ab_format, int a_mn, int b_mn, int M, int N) {
   return (1u << 4) | ((uint32_t)ab_format << 7) | ((uint32_t)ab_format << 10) | ((uint32_t)a_mn << 15) |
          ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// ---------------------------------------------------------------------------
+// bulk stores and copies of this thread
+// ---------------------------------------------------------------------------
+
+// Byte offset of element (r, c) of a staged 32x32 block with 64-byte rows
+// and the TMA 64-byte swizzle (16-byte chunk index XOR (r / 2) % 4).
+__device__ __forceinline__ uint32_t sw64(int r, int c) {
+  return (uint32_t)(r * 64 + ((((c >> 3) ^ (r >> 1)) & 3) << 4) + ((c & 7) << 1));
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the last group (or all) have read their source; all have been written.
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Generic-proxy accesses to this CTA's shared memory before the tensor core or a bulk copy touches it.
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// leaving with nothing in flight
+// ---------------------------------------------------------------------------
+
+// Drains (in-flight copies and MMAs before exit) use their own bound, so that
+// a tiny configurable wait budget never lets a CTA exit with work in flight.
+constexpr uint64_t DRAIN_NS = 1000000000ull;
+
+// Spin (bounded) until the phase with this parity completed; for drains.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
+  const uint32_t addr = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(addr, parity)) {
+    if (globaltimer_ns() - t0 > DRAIN_NS) {
+      report(status, MUON_ERR_TIMEOUT);
+      break;
+    }
+  }
+}
+
+// CTA-pair early exit: wait until every operand copy that either CTA issued
+// has landed, so that no copy writes into shared memory (or signals a
+// barrier) after the pair has left. The copies of both CTAs complete on the
+// leader's full[] barriers; `cnt` holds how many k-blocks each producer
+// issued (leader A, leader B, follower A, follower B). A producer issues
+// k-block j only after the MMAs consumed k-block j - STAGES, which needed
+// every producer's copies of it, so all k-blocks before max(cnt) - STAGES
+// have landed and each of the last STAGES k-blocks occupies its own stage.
+// For those, the barrier is settled for the copies that were never issued
+// (the missing transaction bytes, or the leader's arrival with the bytes that
+// were issued), then waited on with the drain bound. Cf: the kernel's STAGES,
+// A_STAGE, B_STAGE (bytes of a CTA's copies) and TX_BYTES (both CTAs').
+template <typename Cf>
+__device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
+  constexpr int STAGES = Cf::STAGES;
+  const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
+  const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
+  int hi = 0;
+  for (int x = 0; x < 4; ++x) hi = c[x] > hi ? c[x] : hi;
+  for (int j = hi > STAGES ? hi - STAGES : 0; j < hi; ++j) {
+    uint32_t issued = 0;
+    for (int x = 0; x < 4; ++x)
+      if (j < c[x]) issued += bytes[x];
+    uint64_t* bar = &full[j % STAGES];
+    if (j < c[0]) {
+      // the leader's A producer arrived, expecting both CTAs' bytes
+      if (issued < (uint32_t)Cf::TX_BYTES) mbar_complete_tx(bar, Cf::TX_BYTES - issued);
+    } else {
+      mbar_arrive_expect_tx(bar, issued);
+    }
+    drain_wait(bar, (uint32_t)((j / STAGES) & 1), status);
+  }
 }
 
 }  // namespace muon

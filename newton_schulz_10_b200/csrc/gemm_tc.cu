@@ -83,9 +83,6 @@ constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int TMEM_COLS = 512;
 constexpr int EPI_BLOCK = 32 * 32 * 2;             // one staged 32x32 block of bf16/fp16, 64-byte rows
 constexpr int EPI_BUF = 2 * EPI_BLOCK;             // per epilogue warp: direct block + mirrored block
-// Drains (in-flight copies and MMAs before exit) use their own bound, so that
-// a tiny configurable wait budget never lets a CTA exit with work in flight.
-constexpr uint64_t DRAIN_NS = 1000000000ull;
 
 template <int PAIR, int BN, int PL = 1>
 struct Cfg {
@@ -203,20 +200,6 @@ __device__ __forceinline__ float powi(float s, int p) {
   return r;
 }
 
-// Byte offset of element (r, c) of a staged 32x32 block with 64-byte rows
-// and the TMA 64-byte swizzle (16-byte chunk index XOR (r / 2) % 4).
-__device__ __forceinline__ uint32_t sw64(int r, int c) {
-  return (uint32_t)(r * 64 + ((((c >> 3) ^ (r >> 1)) & 3) << 4) + ((c & 7) << 1));
-}
-
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
-               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Wait until at most n (0..4) of this thread's most recent bulk groups are
 // still in flight, i.e. every older group has completed.
 __device__ __forceinline__ void bulk_wait_upto(int n) {
@@ -228,20 +211,6 @@ __device__ __forceinline__ void bulk_wait_upto(int n) {
     default: asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); break;
   }
 }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Spin (bounded) until the phase with this parity completed; for drains.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
-  const uint32_t addr = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(addr, parity)) {
-    if (globaltimer_ns() - t0 > DRAIN_NS) {
-      report(status, MUON_ERR_TIMEOUT);
-      break;
-    }
-  }
-}
-
 // Fused chain: completion counters in global memory. A finished tile's
 // stores are complete (bulk_wait0) and fenced for the async proxy before the
 // release increment; a waiter's acquire load is followed by a proxy fence
@@ -284,40 +253,6 @@ __device__ __forceinline__ bool wait_dep(const Params& p, const Job& g, int b, v
   }
   fence_proxy_async_global();
   return true;
-}
-
-// CTA-pair early exit: wait until every operand copy that either CTA issued
-// has landed, so that no copy writes into shared memory (or signals a
-// barrier) after the pair has left. The copies of both CTAs complete on the
-// leader's full[] barriers; `cnt` holds how many k-blocks each producer
-// issued (leader A, leader B, follower A, follower B). A producer issues
-// k-block j only after the MMAs consumed k-block j - STAGES, which needed
-// every producer's copies of it, so all k-blocks before max(cnt) - STAGES
-// have landed and each of the last STAGES k-blocks occupies its own stage.
-// For those, the barrier is settled for the copies that were never issued
-// (the missing transaction bytes, or the leader's arrival with the bytes that
-// were issued), then waited on with the drain bound.
-template <int PAIR, int BN, int PL>
-__device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
-  using Cf = Cfg<PAIR, BN, PL>;
-  constexpr int STAGES = Cf::STAGES;
-  const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
-  const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
-  int hi = 0;
-  for (int x = 0; x < 4; ++x) hi = c[x] > hi ? c[x] : hi;
-  for (int j = hi > STAGES ? hi - STAGES : 0; j < hi; ++j) {
-    uint32_t issued = 0;
-    for (int x = 0; x < 4; ++x)
-      if (j < c[x]) issued += bytes[x];
-    uint64_t* bar = &full[j % STAGES];
-    if (j < c[0]) {
-      // the leader's A producer arrived, expecting both CTAs' bytes
-      if (issued < (uint32_t)Cf::TX_BYTES) mbar_complete_tx(bar, Cf::TX_BYTES - issued);
-    } else {
-      mbar_arrive_expect_tx(bar, issued);
-    }
-    drain_wait(bar, (uint32_t)((j / STAGES) & 1), status);
-  }
 }
 
 template <typename T, int PAIR, int BN, int PL>
@@ -867,7 +802,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     // every producer has published its count and every early stop has
     // reached both abort flags; the follower stays resident (its shared
     // memory receives its own copies) until the leader's drain ends
-    if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<PAIR, BN, PL>(full, issued_cnt, p.status);
+    if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<Cf>(full, issued_cnt, p.status);
     __syncwarp();
     cluster_sync();
   }

@@ -61,7 +61,6 @@ constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int TMEM_COLS = 512;
 constexpr int ACC_COLS = 256;
 constexpr int kMaxExperts = 1024;
-constexpr uint64_t DRAIN_NS = 1000000000ull;
 // The tensor core truncates each addition to an fp32 accumulator, which
 // shrinks a long sum a little with every instruction (measured: an fp32 dW of
 // 1024 rows is 9.7e-7 off, in proportion to the rows). Sums into fp32 outputs
@@ -193,59 +192,6 @@ __device__ __forceinline__ int parts_of(int nkb) {
   if (MODE == DW && std::is_same<O, float>::value && nkb > kPartBlocks) return (nkb + kPartBlocks - 1) / kPartBlocks;
   return 1;
 }
-
-__device__ __forceinline__ uint32_t sw64(int r, int c) {
-  return (uint32_t)(r * 64 + ((((c >> 3) ^ (r >> 1)) & 3) << 4) + ((c & 7) << 1));
-}
-
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
-  const uint32_t addr = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(addr, parity)) {
-    if (globaltimer_ns() - t0 > DRAIN_NS) {
-      report(status, MUON_ERR_TIMEOUT);
-      break;
-    }
-  }
-}
-
-// Early exit of a pair: wait until every operand copy that either CTA issued
-// has landed. cnt: k-blocks issued by the leader's M-side and N-side producer
-// and the follower's. Blocks before max(cnt) - STAGES have been consumed;
-// each later one occupies its own stage, whose barrier is settled for the
-// copies that were never issued and then waited on.
-template <typename O, int MODE, int NT>
-__device__ void settle_pair_copies(uint64_t* full, const volatile int* cnt, int* status) {
-  using Cf = Cfg<O, MODE, NT>;
-  const int c[4] = {cnt[0], cnt[1], cnt[2], cnt[3]};
-  const uint32_t bytes[4] = {Cf::A_STAGE, Cf::B_STAGE, Cf::A_STAGE, Cf::B_STAGE};
-  int hi = 0;
-  for (int x = 0; x < 4; ++x) hi = c[x] > hi ? c[x] : hi;
-  for (int j = hi > Cf::STAGES ? hi - Cf::STAGES : 0; j < hi; ++j) {
-    uint32_t issued = 0;
-    for (int x = 0; x < 4; ++x)
-      if (j < c[x]) issued += bytes[x];
-    uint64_t* bar = &full[j % Cf::STAGES];
-    if (j < c[0]) {
-      if (issued < (uint32_t)Cf::TX_BYTES) mbar_complete_tx(bar, Cf::TX_BYTES - issued);
-    } else {
-      mbar_arrive_expect_tx(bar, issued);
-    }
-    drain_wait(bar, (uint32_t)((j / Cf::STAGES) & 1), status);
-  }
-}
-
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
-               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// This thread's bulk stores: all but the last one (or all) have read their source; all have been written.
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Sixteen bytes of row `lane` of a staged 32 x 32 block: chunk k, swizzled as
 // the block's tensor map has it (128-byte rows of fp32, 64-byte of 16 bits).
@@ -740,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1) grouped_kernel(const __grid_consta
   __syncwarp();
   cluster_sync();  // no CTA leaves while its pair still signals it
   tc_fence_after();
-  if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<O, MODE, NT>(full, issued_cnt, p.status);
+  if (rank == 0 && threadIdx.x == 0 && *abort_flag) settle_pair_copies<Cf>(full, issued_cnt, p.status);
   __syncwarp();
   cluster_sync();
   if (warp == 2) tmem_dealloc_pair(tmem_base, TMEM_COLS);

@@ -55,7 +55,6 @@ namespace res {
 constexpr int THREADS = 256;
 constexpr int WARPS = THREADS / 32;
 constexpr int TMEM_COLS = 512;
-constexpr uint64_t DRAIN_NS = 1000000000ull;
 
 struct Params {
   StackMat m;
@@ -86,8 +85,6 @@ __device__ __forceinline__ void st_cluster_f64(uint32_t a, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
-// generic-proxy accesses to this CTA's shared memory before the tensor core or a bulk copy touches it
-__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -96,17 +93,6 @@ __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16])
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, int* status) {
-  const uint32_t addr = smem_u32(bar);
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(addr, parity)) {
-    if (globaltimer_ns() - t0 > DRAIN_NS) {
-      report(status, MUON_ERR_TIMEOUT);
-      break;
-    }
-  }
 }
 
 // Byte offset of 16-byte chunk ch (8 columns) of row r in a 64-column group.
@@ -359,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     if (!mbar_wait_bounded(b, par, abort_flag, p.timeout_ns, p.status)) drain_wait(b, par, p.status);
   };
   auto products = [&](auto issue) {
-    fence_operands();
+    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -441,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
     }
     if (C > 1) {
       const uint32_t part = (uint32_t)(rows_per * p.np * 4);
-      fence_operands();
+      fence_async_smem();
       tc_fence_before();
       __syncthreads();
       if (warp == 0) {
@@ -455,8 +441,8 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
           // has added what came in the last step: rows of A from it followed.
           copy_cluster(mapa_shared(smem_u32(R) + rank * part, (uint32_t)lane), a_a + lane * part, part,
                        mapa_shared(smem_u32(sums), (uint32_t)lane));
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          bulk_commit();
+          bulk_wait_read0();
         }
         __syncwarp();  // all of this CTA's copies have been read: its A may be overwritten
         if (lane < C) arrive_cluster(mapa_shared(smem_u32(sums), (uint32_t)lane));
@@ -483,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
         const uint32_t w = (uint32_t)((c0 >> 6) * group) + at(rank * rows_per + lr, (c0 & 63) >> 3);
         put8<T, 2>(A + w, Al + w, v);
       }
-      fence_operands();
+      fence_async_smem();
       __syncthreads();
       // and to the peers: every CTA's partial sums have left its A
       const int pieces = 2 * a_plane / group;  // groups of both planes, contiguous
@@ -493,13 +479,13 @@ __global__ void __launch_bounds__(THREADS, 1) stack_resident(const __grid_consta
         const uint32_t o = a_a + (i - to * pieces) * group + rank * rows_per * 128;
         copy_cluster(mapa_shared(o, (uint32_t)to), o, (uint32_t)(rows_per * 128), mapa_shared(smem_u32(rows), (uint32_t)to));
       }
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      bulk_commit();
       if (tid == 0) mbar_complete_tx(rows, (uint32_t)(pieces * rows_per * 128));  // its own are there
       wait_for(rows, odd);
       // What has arrived says nothing of what this thread has sent: B' takes the
       // place of these rows once every copy has read them (the barrier ahead of
       // the next product makes that every thread's).
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      bulk_wait_read0();
     }
     // B' = a I + b A + c A A, in A's place (every thread rewrites what it read)
     products([&](uint32_t on) {
