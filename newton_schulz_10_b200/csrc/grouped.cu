@@ -32,10 +32,11 @@
 // parts, one work unit each, whose fp32 sums go to the workspace (at most one
 // per CTA pair); a second launch adds them in order.
 //
-// The issuing roles are whole warps (common.cuh: 491 -> 444 us for 32768 rows
-// of 2048 into 64 x 4096). An operand is one copy per k-block (an MN-major
-// one, 64 columns wide by its swizzle, through a map that has the 64-column
-// blocks as a dimension of their own).
+// The issuing roles are whole warps (common.cuh: a tenth less time for 32768
+// rows of 2048 into 64 x 4096, both forms in turn on one GPU; in a loop, at the
+// power cap, that product takes 510 to 545 us). An operand is one copy per
+// k-block (an MN-major one, 64 columns wide by its swizzle, through a map that
+// has the 64-column blocks as a dimension of their own).
 //
 // Every wait is bounded as in the Newton-Schulz GEMM; offsets are clamped to
 // 0..tokens before use, and a decreasing or out-of-range entry is reported as
