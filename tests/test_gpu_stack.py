@@ -612,3 +612,17 @@ def test_status_of_stacks_without_elements(cuda):
         step = mu.StackStep([mu.Stack(gauss(s, 1), gauss(s, 2), gauss(s, 3)) for s in stacks], mu.stack_params(), ws=dirty.clone())
         step()
         assert step.device_status() == mu.OK
+
+
+@pytest.mark.parametrize("kind", ["gauss", "spectrum"])
+@pytest.mark.parametrize("shape", [(1, 4096, 4096), (1, 256, 16384), (2, 2048, 1024)], ids=str)
+def test_two_planes_of_long_sums(cuda, shape, kind):
+    """The largest matrices, with the tolerance of test_two_planes_of_larger_stacks: here most of it is the sums' own."""
+    longer, shorter = max(shape[1:]), min(shape[1:])
+    M = (gauss if kind == "gauss" else spectrum)(shape, 141, 1e-3)
+    W = torch.zeros_like(M)
+    step = mu.stack_step([mu.Stack(W, M)], mu.stack_params(lr=1.0, scale=-1.0, ns=mu.ns_params(compute=mu.F16X2)))
+    assert step.device_status() == mu.OK
+    want = polar(M)
+    for i in range(shape[0]):
+        assert rel(W[i], want[i]) <= TOL[mu.F16X2] + 5 * 2 * (longer + 2 * shorter) / 16 * 2.0 ** -23 / 3, i
